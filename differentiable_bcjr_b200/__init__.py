@@ -12,6 +12,13 @@ the calls raise.
   bcjr_dense_forward / bcjr_dense_backward            (fully connected trellis)
   bcjr_dense_backward(..., want_grad_log_trans=True)  (also dL/dLambda, tensor cores)
   SoftTrellisQuant, DenseTrellisQuant                 torch.autograd.Function
+
+and, for training and serving quantised layers (layer.py; C ABI in include/bcjr_layer.h):
+
+  adamw_step(params, grads, exp_avg, exp_avg_sq, step) one AdamW step of many tensors, states in 32 or 8 bits
+  int4_quantize(w) / int4_matmul(x, packed, scales)   4-bit weights with group scales
+  trellis_pack(states, state_bits, k)                 hard-decoded states at k bits a weight
+  trellis_matmul(x, packed, codebook, ...)            products with packed trellis weights
 """
 from __future__ import annotations
 
@@ -26,6 +33,7 @@ __all__ = [
     "SoftTrellisQuant", "soft_quantize", "DenseTrellisQuant", "dense_soft_quantize", "bcjr_forward_static_scratch",
     "static_scratch_status", "probe_xu", "probe_mma_tf32", "probe_dsmem", "OP_FORWARD", "OP_BACKWARD", "OP_VITERBI",
     "OP_DENSE_FORWARD", "OP_DENSE_BACKWARD", "OP_DENSE_BACKWARD_LAMBDA", "STATUS",
+    "adamw_step", "adamw_state", "int4_quantize", "int4_matmul", "trellis_pack", "trellis_words", "trellis_matmul",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libbcjr.so")
@@ -72,6 +80,12 @@ _SIGS = {
     "bcjr_probe_dsmem": (_I, [_I, _I, _P, _P, _I, _P]),
     "bcjr_probe_dsmem_bulk": (_I, [_I, _I, _I, _P, _P, _I, _P]),
     "bcjr_version": (_I, []),
+    # bcjr_layer.h
+    "bcjr_adamw_step": (_I, [_P, _I, _I, _I, _I, _P, _P, _P, _P, _P]),
+    "bcjr_int4_quantize": (_I, [_P, _I, _I, _I, _I, _P, _P, _I, _P, _P]),
+    "bcjr_int4_matmul": (_I, [_P, _I, _I, _I, _I, _P, _P, _I, _P, _I, _P, _P]),
+    "bcjr_trellis_pack": (_I, [_P, _I, _I, _I, _I, _P, _P, _P]),
+    "bcjr_trellis_matmul": (_I, [_P, _I, _I, _I, _I, _P, _P, _I, _I, _I, _I, _P, _I, _P, _P]),
 }
 
 
@@ -462,3 +476,7 @@ def probe_dsmem(reps: int = 4, rounds: int = 100, clusters: int = 0, device=None
     r = sorted(out / float(v) for v in cycles.cpu().tolist())
     return {"bytes_per_clk_per_sm": r[len(r) // 2], "min": r[0], "max": r[-1], "ctas": 4 * ncl}
 
+
+
+from .layer import (adamw_state, adamw_step, int4_matmul, int4_quantize, trellis_matmul, trellis_pack,  # noqa: E402
+                    trellis_words)

@@ -1,0 +1,363 @@
+// adamw.cu -- one AdamW step of many tensors in one launch (bcjr_adamw_step).
+//
+// An elementwise pass: every byte of p, g and the two states is read once and
+// p and the states are written once, so memory bandwidth bounds it (28 B an
+// element for float32 with 32-bit states, 10.06 B for bf16 with 8-bit ones).
+// The flat states are cut into blocks of 256 elements, the blocks that 8-bit
+// scales belong to; a warp takes one block at a time, 8 elements a lane, and
+// finds its tensor by bisection in a table that travels as a kernel
+// parameter, so a call needs no device memory of its own and no copy.
+#include <cmath>
+#include <cstring>
+
+#include "layer_util.cuh"
+
+namespace {
+
+using namespace bcjr;
+
+constexpr int kBlock = 256;     // elements of a state block
+constexpr int kWarps = 8;
+constexpr float kTiny = 0x1p-100f;
+
+struct Scalars {
+  float b1, c1, b2, c2, eps, decay;  // c = 1 - b, decay = 1 - lr wd
+  float lr_bc1, inv_sqrt_bc2;        // lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
+  uint32_t mix;                      // of step and seed
+};
+
+template <int CAP>
+struct Table {
+  void* p[CAP];
+  const void* g[CAP];
+  int64_t numel[CAP];
+  int first_block[CAP];  // relative to the launch's first block
+  int n;
+  int blocks;            // of the launch
+};
+
+struct Common {
+  void* first;
+  void* second;
+  float* scales;           // [2][all blocks] (8-bit states)
+  size_t all_blocks;
+  size_t block0;           // of the launch within the flat states
+  const int64_t* step_ptr;
+  const float* grad_scale;
+  double lr, beta1, beta2;
+  uint32_t seed;
+  Scalars s;
+};
+
+__host__ __device__ inline uint32_t mix_of(uint32_t step, uint32_t seed) {
+  return step * 0x632BE5ABu + seed * 0x85157AF5u;
+}
+
+__host__ __device__ inline void bias_scalars(double lr, double b1, double b2, double t, Scalars& s) {
+  s.lr_bc1 = static_cast<float>(lr / (1.0 - pow(b1, t)));
+  s.inv_sqrt_bc2 = static_cast<float>(1.0 / sqrt(1.0 - pow(b2, t)));
+}
+
+// 32 bits a (step, seed, element): 16 for either rounding.
+__device__ __forceinline__ uint32_t hash_bits(uint32_t element, uint32_t mix) {
+  uint32_t h = element * 0x9E3779B1u + mix;
+  h = (h ^ (h >> 15)) * 0x2C1B3C6Du;
+  h = (h ^ (h >> 12)) * 0x297A2D39u;
+  return h ^ (h >> 15);
+}
+
+// Magnitude code of t in [0, 448]: scaled by 2^-120 a float's exponent field
+// is e4m3's, so the code is the float's bits cut after three mantissa bits;
+// the 20 bits that fall away decide the rounding together with `rnd`.
+__device__ __forceinline__ uint32_t e4m3_code(float t, uint32_t rnd) {
+  return min((__float_as_uint(__fmul_rn(t, 0x1p-120f)) + rnd) >> 20, 0x7Eu);
+}
+
+__device__ __forceinline__ float e4m3_value(uint32_t byte) {
+  const uint32_t mag = (byte & 0x7Fu) << 20;
+  return __uint_as_float(__float_as_uint(__fmul_rn(__uint_as_float(mag), 0x1p120f)) | ((byte & 0x80u) << 24));
+}
+
+__device__ __forceinline__ float sqrt_approx(float v) {  // within 2^-23 of the root, denormals included
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// Which elements of its block a lane holds: COALESCED 4 at 4 lane and 4 at
+// 128 + 4 lane (16-byte loads of float32); PACKED 8 at 8 lane (16-byte loads
+// of 16-bit types); STRIDED lane, lane + 32, ... one by one, for tensors that
+// are not 16-byte aligned and for the last block of a tensor.
+enum Map { COALESCED, PACKED, STRIDED };
+
+template <Map MAP>
+__device__ __forceinline__ int element_of(int lane, int i) {
+  if (MAP == COALESCED) return (i >> 2) * 128 + lane * 4 + (i & 3);
+  if (MAP == PACKED) return lane * 8 + i;
+  return i * 32 + lane;
+}
+
+template <int BYTES>
+struct Raw;
+template <>
+struct Raw<4> { using type = uint32_t; };
+template <>
+struct Raw<8> { using type = uint2; };
+template <>
+struct Raw<16> { using type = uint4; };
+
+template <typename T, Map MAP>
+__device__ __forceinline__ void load8(const T* base, int lane, int limit, T (&v)[8]) {
+  if constexpr (MAP == STRIDED) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = element_of<MAP>(lane, i);
+      if (e < limit) v[i] = base[e];
+      else memset(&v[i], 0, sizeof(T));
+    }
+  } else {
+    constexpr int RUN = MAP == PACKED ? 8 : 4;
+    static_assert(RUN * sizeof(T) <= 16, "one vector access a run");
+    using V = typename Raw<RUN * sizeof(T)>::type;
+#pragma unroll
+    for (int i = 0; i < 8; i += RUN) {
+      const V x = *reinterpret_cast<const V*>(base + element_of<MAP>(lane, i));
+      memcpy(&v[i], &x, sizeof(V));
+    }
+  }
+}
+
+template <typename T, Map MAP>
+__device__ __forceinline__ void store8(T* base, int lane, int limit, const T (&v)[8]) {
+  if constexpr (MAP == STRIDED) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = element_of<MAP>(lane, i);
+      if (e < limit) base[e] = v[i];
+    }
+  } else {
+    constexpr int RUN = MAP == PACKED ? 8 : 4;
+    using V = typename Raw<RUN * sizeof(T)>::type;
+#pragma unroll
+    for (int i = 0; i < 8; i += RUN) {
+      V x;
+      memcpy(&x, &v[i], sizeof(V));
+      *reinterpret_cast<V*>(base + element_of<MAP>(lane, i)) = x;
+    }
+  }
+}
+
+// One block of one tensor.  `limit`: elements of the block that exist.
+template <typename P, typename G, int BITS, Map MAP>
+__device__ __forceinline__ void block_step(P* p, const G* g, const Common& c, const Scalars& s, float gs,
+                                           size_t block, int lane, int limit) {
+  using S = typename std::conditional<BITS == 32, float, uint8_t>::type;
+  S* const first = static_cast<S*>(c.first) + block * kBlock;
+  S* const second = static_cast<S*>(c.second) + block * kBlock;
+  P pv[8];
+  G gv[8];
+  S a[8], b[8];
+  load8<S, MAP>(first, lane, kBlock, a);
+  load8<S, MAP>(second, lane, kBlock, b);
+  load8<G, MAP>(g, lane, limit, gv);
+  load8<P, MAP>(p, lane, limit, pv);
+  float sa = 1.f, sb = 1.f;
+  if constexpr (BITS == 8) {
+    sa = c.scales[block];
+    sb = c.scales[c.all_blocks + block];
+  }
+  float m[8], r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    // each product and sum rounded on its own, so that a rounding decision of
+    // the 8-bit codes does not depend on how the compiler contracts them
+    const float gr = __fmul_rn(to_f32(gv[i]), gs);
+    float v;
+    if constexpr (BITS == 32) {
+      m[i] = a[i];
+      v = b[i];
+    } else {
+      m[i] = __fmul_rn(e4m3_value(a[i]), sa);
+      const float r0 = __fmul_rn(e4m3_value(b[i]), sb);
+      v = __fmul_rn(r0, r0);
+    }
+    m[i] = __fadd_rn(__fmul_rn(m[i], s.b1), __fmul_rn(gr, s.c1));
+    v = __fadd_rn(__fmul_rn(v, s.b2), __fmul_rn(__fmul_rn(gr, gr), s.c2));
+    r[i] = sqrt_approx(v);
+    const float step = __fdividef(m[i], fmaf(r[i], s.inv_sqrt_bc2, s.eps));
+    pv[i] = from_f32<P>(fmaf(-s.lr_bc1, step, to_f32(pv[i]) * s.decay));
+    if constexpr (BITS == 32) {
+      a[i] = m[i];
+      b[i] = v;
+    }
+  }
+  store8<P, MAP>(p, lane, limit, pv);
+  if constexpr (BITS == 8) {
+    // the order of the absolute values' bits is that of the values, NaN above all
+    uint32_t ta = 0, tb = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (MAP == STRIDED && element_of<MAP>(lane, i) >= limit) m[i] = r[i] = 0.f;
+      ta = max(ta, __float_as_uint(m[i]) & 0x7FFFFFFFu);
+      tb = max(tb, __float_as_uint(r[i]) & 0x7FFFFFFFu);
+    }
+    const float top_a = __uint_as_float(__reduce_max_sync(~0u, ta));
+    const float top_b = __uint_as_float(__reduce_max_sync(~0u, tb));
+    const bool held_a = !(top_a < kTiny), held_b = !(top_b < kTiny);
+    const float inv_a = held_a ? __fdiv_rn(448.f, top_a) : 0.f, inv_b = held_b ? __fdiv_rn(448.f, top_b) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t h = hash_bits(static_cast<uint32_t>(block * kBlock) + element_of<MAP>(lane, i), s.mix);
+      const uint32_t ca = e4m3_code(__fmul_rn(fabsf(m[i]), inv_a), ((h >> 16) << 4) | 8u);
+      const uint32_t cb = e4m3_code(__fmul_rn(r[i], inv_b), ((h & 0xFFFFu) << 4) | 8u);
+      a[i] = static_cast<uint8_t>(ca | (m[i] < 0.f ? 0x80u : 0u));
+      b[i] = static_cast<uint8_t>(held_b && r[i] > 0.f ? max(cb, 1u) : cb);
+    }
+    if (lane == 0) {
+      c.scales[block] = held_a ? __fdiv_rn(top_a, 448.f) : 0.f;
+      c.scales[c.all_blocks + block] = held_b ? __fdiv_rn(top_b, 448.f) : 0.f;
+    }
+  }
+  store8<S, MAP>(first, lane, MAP == STRIDED ? limit : kBlock, a);
+  store8<S, MAP>(second, lane, MAP == STRIDED ? limit : kBlock, b);
+}
+
+template <typename P, typename G, int BITS, int CAP>
+__global__ void __launch_bounds__(kWarps * 32) adamw_kernel(const __grid_constant__ Table<CAP> t,
+                                                            const __grid_constant__ Common c) {
+  Scalars s = c.s;
+  if (c.step_ptr) {  // uniform: the step count is only known now
+    __shared__ Scalars shared;
+    if (threadIdx.x == 0) {
+      const int64_t step = *c.step_ptr;
+      shared = c.s;
+      bias_scalars(c.lr, c.beta1, c.beta2, static_cast<double>(step), shared);
+      shared.mix = mix_of(static_cast<uint32_t>(step), c.seed);
+    }
+    __syncthreads();
+    s = shared;
+  }
+  const float gs = c.grad_scale ? *c.grad_scale : 1.f;
+  const int lane = threadIdx.x & 31;
+  const int b = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (b >= t.blocks) return;
+  int lo = 0, hi = t.n - 1;  // the last tensor that starts at or before b
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.first_block[mid] <= b) lo = mid;
+    else hi = mid - 1;
+  }
+  if (!t.g[lo]) return;
+  const int64_t at = static_cast<int64_t>(b - t.first_block[lo]) * kBlock;
+  const int64_t left = t.numel[lo] - at;
+  P* const p = static_cast<P*>(t.p[lo]) + at;
+  const G* const g = static_cast<const G*>(t.g[lo]) + at;
+  const size_t block = c.block0 + b;
+  constexpr Map FULL = (BITS == 8 && sizeof(P) == 2 && sizeof(G) == 2) ? PACKED : COALESCED;
+  if (left >= kBlock && ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(g)) & 15) == 0)
+    block_step<P, G, BITS, FULL>(p, g, c, s, gs, block, lane, kBlock);
+  else
+    block_step<P, G, BITS, STRIDED>(p, g, c, s, gs, block, lane, left < kBlock ? static_cast<int>(left) : kBlock);
+}
+
+template <typename P, typename G, int BITS, int CAP>
+bcjr_status launch(const bcjr_adamw_tensor* ts, int n, Common& c, cudaStream_t stream) {
+  Table<CAP> t;
+  t.n = 0;
+  int64_t blocks = 0;
+  for (int i = 0; i <= n; ++i) {
+    const int64_t more = i < n ? (ts[i].numel + kBlock - 1) / kBlock : 0;
+    // a launch's blocks are counted in an int
+    if (t.n > 0 && (i == n || t.n == CAP || blocks + more > (int64_t{1} << 30))) {
+      t.blocks = static_cast<int>(blocks);
+      const unsigned grid = static_cast<unsigned>((blocks + kWarps - 1) / kWarps);
+      adamw_kernel<P, G, BITS, CAP><<<grid, kWarps * 32, 0, stream>>>(t, c);
+      const bcjr_status st = launched();
+      if (st != BCJR_OK) return st;
+      c.block0 += static_cast<size_t>(blocks);
+      t.n = 0;
+      blocks = 0;
+    }
+    if (i == n || more == 0) continue;
+    t.p[t.n] = ts[i].param;
+    t.g[t.n] = ts[i].grad;
+    t.numel[t.n] = ts[i].numel;
+    t.first_block[t.n] = static_cast<int>(blocks);
+    ++t.n;
+    blocks += more;
+  }
+  return BCJR_OK;
+}
+
+// Tables of 128 tensors fit the classic 4 KB of kernel parameters, which are
+// cheaper to launch with; 1024 tensors take 28 KB.
+template <typename P, typename G, int BITS>
+bcjr_status launch_any(const bcjr_adamw_tensor* ts, int n, Common& c, cudaStream_t stream) {
+  return n <= 128 ? launch<P, G, BITS, 128>(ts, n, c, stream) : launch<P, G, BITS, 1024>(ts, n, c, stream);
+}
+
+template <typename P, typename G>
+bcjr_status launch_bits(const bcjr_adamw_tensor* ts, int n, int bits, Common& c, cudaStream_t stream) {
+  return bits == 8 ? launch_any<P, G, 8>(ts, n, c, stream) : launch_any<P, G, 32>(ts, n, c, stream);
+}
+
+}  // namespace
+
+extern "C" bcjr_status bcjr_adamw_step(const bcjr_adamw_tensor* tensors, int n_tensors, int param_dtype,
+                                       int grad_dtype, int state_bits, void* first, void* second, float* scales,
+                                       const bcjr_adamw_options* o, bcjr_stream_t stream) {
+  if (n_tensors < 0 || (n_tensors > 0 && !tensors) || !o) return BCJR_ERR_INVALID_ARG;
+  if (!dtype_ok(param_dtype) || !dtype_ok(grad_dtype)) return BCJR_ERR_INVALID_ARG;
+  if (state_bits != 8 && state_bits != 32) return BCJR_ERR_UNSUPPORTED;
+  if (param_dtype != BCJR_F32 && grad_dtype != BCJR_F32 && grad_dtype != param_dtype) return BCJR_ERR_UNSUPPORTED;
+  if (!std::isfinite(o->lr) || o->lr < 0 || !(o->beta1 >= 0 && o->beta1 < 1) || !(o->beta2 >= 0 && o->beta2 < 1) ||
+      !(o->eps >= 0) || !std::isfinite(o->eps) || !std::isfinite(o->weight_decay) || o->weight_decay < 0)
+    return BCJR_ERR_INVALID_ARG;
+  if (!o->step_ptr && o->step < 1) return BCJR_ERR_INVALID_ARG;
+  int64_t blocks = 0;
+  for (int i = 0; i < n_tensors; ++i) {
+    const bcjr_adamw_tensor& t = tensors[i];
+    if (t.numel < 0 || t.numel > (int64_t{1} << 37)) return BCJR_ERR_INVALID_ARG;
+    if (t.numel > 0 && (!t.param || !ptr_aligned(t.param, dtype_size(param_dtype)) ||
+                        !ptr_aligned(t.grad, dtype_size(grad_dtype))))
+      return BCJR_ERR_INVALID_ARG;
+    blocks += (t.numel + kBlock - 1) / kBlock;
+  }
+  if (blocks == 0) return BCJR_OK;
+  if (!first || !second || !ptr_aligned(first, 16) || !ptr_aligned(second, 16)) return BCJR_ERR_INVALID_ARG;
+  if ((state_bits == 8) != (scales != nullptr) || !ptr_aligned(scales, 4) || !ptr_aligned(o->grad_scale, 4) ||
+      !ptr_aligned(o->step_ptr, 8))
+    return BCJR_ERR_INVALID_ARG;
+  Common c = {};
+  c.first = first;
+  c.second = second;
+  c.scales = scales;
+  c.all_blocks = static_cast<size_t>(blocks);
+  c.step_ptr = o->step_ptr;
+  c.grad_scale = o->grad_scale;
+  c.lr = o->lr;
+  c.beta1 = o->beta1;
+  c.beta2 = o->beta2;
+  c.seed = o->seed;
+  c.s.b1 = static_cast<float>(o->beta1);
+  c.s.c1 = static_cast<float>(1.0 - o->beta1);
+  c.s.b2 = static_cast<float>(o->beta2);
+  c.s.c2 = static_cast<float>(1.0 - o->beta2);
+  c.s.eps = static_cast<float>(o->eps);
+  c.s.decay = static_cast<float>(1.0 - o->lr * o->weight_decay);
+  if (!o->step_ptr) {
+    bias_scalars(o->lr, o->beta1, o->beta2, static_cast<double>(o->step), c.s);
+    c.s.mix = mix_of(static_cast<uint32_t>(o->step), o->seed);
+  }
+  cudaStream_t s = as_stream(stream);
+  if (param_dtype == BCJR_F32) {
+    if (grad_dtype == BCJR_F32) return launch_bits<float, float>(tensors, n_tensors, state_bits, c, s);
+    if (grad_dtype == BCJR_F16) return launch_bits<float, __half>(tensors, n_tensors, state_bits, c, s);
+    return launch_bits<float, __nv_bfloat16>(tensors, n_tensors, state_bits, c, s);
+  }
+  if (param_dtype == BCJR_F16)
+    return grad_dtype == BCJR_F32 ? launch_bits<__half, float>(tensors, n_tensors, state_bits, c, s)
+                                  : launch_bits<__half, __half>(tensors, n_tensors, state_bits, c, s);
+  return grad_dtype == BCJR_F32 ? launch_bits<__nv_bfloat16, float>(tensors, n_tensors, state_bits, c, s)
+                                : launch_bits<__nv_bfloat16, __nv_bfloat16>(tensors, n_tensors, state_bits, c, s);
+}

@@ -1,0 +1,57 @@
+// layer_util.cuh -- element types and small helpers of the calls in bcjr_layer.h.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "bcjr_layer.h"
+
+namespace bcjr {
+
+inline bool ptr_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+inline bool dtype_ok(int d) { return d == BCJR_F32 || d == BCJR_F16 || d == BCJR_BF16; }
+inline size_t dtype_size(int d) { return d == BCJR_F32 ? 4 : 2; }
+inline bcjr_status launched() { return cudaGetLastError() == cudaSuccess ? BCJR_OK : BCJR_ERR_CUDA; }
+inline cudaStream_t as_stream(bcjr_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
+
+// Multiprocessors of the current device, asked once a device.
+inline int sm_count() {
+  static int known[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if (known[dev] == 0) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    known[dev] = n;
+  }
+  return known[dev];
+}
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// Element i of an array whose type is only known at run time (a uniform branch).
+__device__ __forceinline__ float load_as_f32(const void* p, int dtype, size_t i) {
+  if (dtype == BCJR_F32) return static_cast<const float*>(p)[i];
+  if (dtype == BCJR_F16) return __half2float(static_cast<const __half*>(p)[i]);
+  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+
+__device__ __forceinline__ void store_from_f32(void* p, int dtype, size_t i, float v) {
+  if (dtype == BCJR_F32) static_cast<float*>(p)[i] = v;
+  else if (dtype == BCJR_F16) static_cast<__half*>(p)[i] = __float2half_rn(v);
+  else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+}
+
+}  // namespace bcjr

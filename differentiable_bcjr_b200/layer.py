@@ -1,0 +1,292 @@
+"""Calls around a quantised layer (C ABI in include/bcjr_layer.h): the AdamW
+step that trains weight preimages and codebooks, the 4-bit group quantiser,
+the packing of hard-decoded trellis states, and products with either kind of
+packed weights.
+
+As in the rest of the binding, tensors must be contiguous CUDA tensors of one
+device, every call is asynchronous on that device's current stream, malformed
+arguments raise before anything is launched, and nothing falls back to
+PyTorch.  The products have no gradient: they serve frozen layers.
+"""
+from __future__ import annotations
+
+from array import array
+import ctypes
+
+import torch
+
+from . import BCJRError, lib
+
+_DTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_raw_stream = torch._C._cuda_getCurrentRawStream
+STATE_BLOCK = 256  # elements of a block of optimiser state
+
+
+def _call(name, index, *args):
+    """The library's call `name` on the current stream of device `index`."""
+    if torch.cuda.current_device() == index:
+        status = getattr(lib(), name)(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = getattr(lib(), name)(*args, _raw_stream(index))
+    if status != 0:
+        raise BCJRError(status, name)
+
+
+def _on_device(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (libbcjr has no CPU path)")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.get_device()
+
+
+def _like(t, name, shape, dtype, index):
+    if _on_device(t, name) != index:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+
+
+def _dtype(t, name):
+    code = _DTYPE.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16, not {t.dtype}")
+    return code
+
+
+class _AdamWOptions(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64),
+                ("step_ptr", ctypes.c_void_p), ("grad_scale", ctypes.c_void_p), ("seed", ctypes.c_uint32)]
+
+
+def adamw_state(params, state_bits=32):
+    """Zeroed states for `adamw_step` on `params`: (exp_avg, exp_avg_sq, scales or None)."""
+    params = list(params)
+    if state_bits not in (8, 32):
+        raise ValueError("state_bits must be 8 or 32")
+    if not params:
+        raise ValueError("there are no parameters")
+    blocks = sum(-(-p.numel() // STATE_BLOCK) for p in params)
+    dev = params[0].device
+    kind = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
+    first = torch.zeros(blocks * STATE_BLOCK, dtype=torch.float32 if state_bits == 32 else torch.uint8, device=dev).view(kind)
+    second = torch.zeros_like(first)
+    return first, second, torch.zeros((2, blocks), device=dev) if state_bits == 8 else None
+
+
+def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0,
+               scales=None, grad_scale=None, seed=0):
+    """One AdamW step of every tensor of `params`, in place, in one launch.
+
+    `params` and `grads` are lists of as many tensors: float32 parameters with
+    gradients of any float type, or 16-bit ones with gradients of the same
+    type or float32.  A gradient may be None: that parameter and its states
+    are left as they are.  The states are flat (see `adamw_state`; tensor i
+    starts at the next multiple of 256 elements): float32, or float8_e4m3fn
+    codes with `scales` float32 [2][blocks].  With 8-bit states `exp_avg_sq`
+    holds the root of the second moment, and codes are rounded stochastically
+    from a hash of `seed`, the step and the element's index.
+
+    `step` counts from 1; it is a number, or an int64 CUDA tensor of one
+    element that the kernel reads (what a captured graph needs: with a number,
+    capture is refused, because every replay would repeat that step).
+    `grad_scale`, a float32 CUDA tensor of one element, multiplies every
+    gradient (clipping or loss scaling without a synchronisation).
+    """
+    n = len(params)
+    if len(grads) != n:
+        raise ValueError(f"{n} parameters and {len(grads)} gradients")
+    if n == 0:
+        return
+    T = torch.Tensor
+    given = [g for g in grads if g is not None]
+    index = params[0].get_device()
+    if index < 0 or {index} != set(map(T.get_device, params)) or not {index} >= set(map(T.get_device, given)):
+        raise ValueError("parameters and gradients must be CUDA tensors of one device (libbcjr has no CPU path)")
+    if not (all(map(T.is_contiguous, params)) and all(map(T.is_contiguous, given))):
+        raise ValueError("parameters and gradients must be contiguous")
+    kind, = _one_dtype(params, "parameters")
+    gkind = _one_dtype(given, "gradients")[0] if given else kind
+    if kind != torch.float32 and gkind not in (torch.float32, kind):
+        raise ValueError(f"{kind} parameters take gradients of {kind} or float32, not {gkind}")
+    numel = list(map(T.numel, params))
+    pp = list(map(T.data_ptr, params))
+    if len(given) == n:
+        gp, gn = list(map(T.data_ptr, grads)), list(map(T.numel, grads))
+        if gn != numel:
+            raise ValueError("every gradient must have as many elements as its parameter")
+    else:
+        gp = [0 if g is None else g.data_ptr() for g in grads]
+        if any(g is not None and g.numel() != m for g, m in zip(grads, numel)):
+            raise ValueError("every gradient must have as many elements as its parameter")
+    size = 4 if kind == torch.float32 else 2
+    spans = sorted(zip(pp, numel))
+    if any(a + m * size > b for (a, m), (b, k) in zip(spans, spans[1:]) if k):
+        raise ValueError("parameters must not overlap")
+    blocks = sum([-(-m // STATE_BLOCK) for m in numel])
+    bits = 32 if scales is None else 8
+    held = torch.float32 if bits == 32 else torch.float8_e4m3fn
+    flat = (blocks * STATE_BLOCK,)
+    _like(exp_avg, "exp_avg", flat, held, index)
+    _like(exp_avg_sq, "exp_avg_sq", flat, held, index)
+    if scales is not None:
+        _like(scales, "scales", (2, blocks), torch.float32, index)
+    o = _AdamWOptions(lr, betas[0], betas[1], eps, weight_decay, 0, None, None, seed & 0xFFFFFFFF)
+    if isinstance(step, T):
+        _like(step, "step", step.shape, torch.int64, index)
+        if step.numel() != 1:
+            raise ValueError("step must have one element")
+        o.step_ptr = step.data_ptr()
+    else:
+        if torch.cuda.is_current_stream_capturing():
+            raise ValueError("a captured step needs its count in a CUDA tensor")
+        o.step = int(step)
+    if grad_scale is not None:
+        _like(grad_scale, "grad_scale", grad_scale.shape, torch.float32, index)
+        if grad_scale.numel() != 1:
+            raise ValueError("grad_scale must have one element")
+        o.grad_scale = grad_scale.data_ptr()
+    table = array("Q", bytes(24 * n))
+    table[0::3] = array("Q", pp)
+    table[1::3] = array("Q", gp)
+    table[2::3] = array("Q", numel)
+    _call("bcjr_adamw_step", index, table.buffer_info()[0], n, _DTYPE[kind], _DTYPE[gkind], bits, exp_avg.data_ptr(),
+          exp_avg_sq.data_ptr(), None if scales is None else scales.data_ptr(), ctypes.byref(o))
+    torch.autograd.graph.increment_version(params)
+
+
+def _one_dtype(ts, name):
+    kinds = {t.dtype for t in ts}
+    if len(kinds) != 1 or not kinds <= _DTYPE.keys():
+        raise ValueError(f"{name} must all be float32, float16 or bfloat16, not {sorted(map(str, kinds))}")
+    return tuple(kinds)
+
+
+def _groups(cols, group_size):
+    if group_size < 0 or (group_size % 128 and group_size not in (32, 64)):
+        raise ValueError("group_size must be 32, 64, a multiple of 128, or 0 for the whole row")
+    return -(-cols // group_size) if group_size else 1
+
+
+def int4_quantize(w, group_size=128, zero_point=False, scale_dtype=None):
+    """w [rows][cols] rounded to 4 bits with one scale a group of `group_size`
+    columns (32, 64, a multiple of 128, or 0 for the whole row).  Returns
+    (packed uint8 [ceil(rows/16)][ceil(cols/128)][1024], scales [groups][rows]
+    of `scale_dtype` (w's by default), zeros uint8 [groups][rows] or None).
+    Symmetric codes stand for -7..7 (8 is zero); with `zero_point` a group's
+    range from its least to its largest value (0 among them) takes codes 0..15.
+    bcjr_layer.h gives the layout of the packed tiles."""
+    index = _on_device(w, "w")
+    if w.dim() != 2 or w.shape[1] < 1:
+        raise ValueError("w must be [rows][cols]")
+    rows, cols = w.shape
+    groups = _groups(cols, group_size)
+    kind = w.dtype if scale_dtype is None else scale_dtype
+    if kind not in _DTYPE:
+        raise ValueError(f"scale_dtype must be float32, float16 or bfloat16, not {kind}")
+    dev = w.device
+    packed = torch.empty((-(-rows // 16), -(-cols // 128), 1024), dtype=torch.uint8, device=dev)
+    scales = torch.empty((groups, rows), dtype=kind, device=dev)
+    zeros = torch.empty((groups, rows), dtype=torch.uint8, device=dev) if zero_point else None
+    _call("bcjr_int4_quantize", index, w.data_ptr(), _dtype(w, "w"), rows, cols, group_size, packed.data_ptr(),
+          scales.data_ptr(), _DTYPE[kind], None if zeros is None else zeros.data_ptr())
+    return packed, scales, zeros
+
+
+def int4_matmul(x, packed, scales, zeros=None, group_size=128, out=None):
+    """x [..., cols] times the transpose of 4-bit weights: [..., rows] of x's
+    type, sums in float32.  `packed`, `scales`, `zeros` and `group_size` as
+    `int4_quantize` gives and takes them."""
+    index = _on_device(x, "x")
+    kind = _dtype(x, "x")
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must be [..., cols]")
+    cols = x.shape[-1]
+    if scales.dim() != 2:
+        raise ValueError("scales must be [groups][rows]")
+    rows = scales.shape[1]
+    _like(scales, "scales", (_groups(cols, group_size), rows), scales.dtype, index)
+    _like(packed, "packed", (-(-rows // 16), -(-cols // 128), 1024), torch.uint8, index)
+    if zeros is not None:
+        _like(zeros, "zeros", scales.shape, torch.uint8, index)
+    shape = x.shape[:-1] + (rows,)
+    if out is None:
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    else:
+        _like(out, "out", shape, x.dtype, index)
+    _call("bcjr_int4_matmul", index, x.data_ptr(), kind, x.numel() // cols, rows, cols, packed.data_ptr(),
+          scales.data_ptr(), _dtype(scales, "scales"), None if zeros is None else zeros.data_ptr(), group_size,
+          out.data_ptr())
+    return out
+
+
+def _trellis(state_bits, k):
+    if not (1 <= k <= 4 and k <= state_bits <= 16):
+        raise ValueError("packed trellis codes need 1 <= k <= 4 and k <= state_bits <= 16")
+
+
+def trellis_words(state_bits, k, seq_len):
+    """32-bit words that a packed sequence of seq_len states takes."""
+    _trellis(state_bits, k)
+    return (seq_len * k + state_bits - k + 31) // 32
+
+
+def trellis_pack(states, state_bits, k, check=False):
+    """Hard-decoded states (int32 [n_seq][seq_len], as `viterbi_decode` gives
+    them) as one bit stream a sequence, k bits a step after the first:
+    int32 [n_seq][trellis_words(state_bits, k, seq_len)].  With `check` the
+    call waits for the GPU and raises if some state does not follow from the
+    one before; without it such a state's upper bits are lost."""
+    index = _on_device(states, "states")
+    if states.dim() != 2 or states.shape[1] < 1 or states.dtype != torch.int32:
+        raise ValueError("states must be int32 [n_seq][seq_len]")
+    n_seq, n = states.shape
+    packed = torch.empty((n_seq, trellis_words(state_bits, k, n)), dtype=torch.int32, device=states.device)
+    bad = torch.zeros(1, dtype=torch.int32, device=states.device) if check else None
+    _call("bcjr_trellis_pack", index, states.data_ptr(), state_bits, k, n, n_seq, packed.data_ptr(),
+          None if bad is None else bad.data_ptr())
+    if check and bad.item():
+        raise ValueError("the states are not a path of the bitshift trellis")
+    return packed
+
+
+def trellis_matmul(x, packed, codebook, state_bits, k, seq_len, scales=None, group_size=0, out=None):
+    """x [..., cols] times the transpose of packed trellis weights: [..., rows]
+    of x's type.  A row's weights are cols / seq_len sequences of `packed`
+    (int32 [rows * cols / seq_len][words], see `trellis_pack`) read through
+    `codebook` [2^state_bits], each times `scales` (float32 [cols /
+    group_size][rows]) when given.  group_size: 0 for one scale a row, a
+    multiple of seq_len that divides cols, or a multiple of 16 that divides
+    seq_len.  Products and sums are float32."""
+    index = _on_device(x, "x")
+    kind = _dtype(x, "x")
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must be [..., cols]")
+    cols = x.shape[-1]
+    if seq_len < 1 or cols % seq_len:
+        raise ValueError("a row must be whole sequences")
+    seqs = cols // seq_len
+    words = trellis_words(state_bits, k, seq_len)
+    if packed.dim() != 2 or packed.shape[0] % seqs:
+        raise ValueError("packed must be [rows * cols / seq_len][words]")
+    rows = packed.shape[0] // seqs
+    _like(packed, "packed", (rows * seqs, words), torch.int32, index)
+    _like(codebook, "codebook", (1 << state_bits,), codebook.dtype, index)
+    if scales is not None:
+        if group_size and not ((group_size % seq_len == 0 and cols % group_size == 0) or
+                               (group_size % 16 == 0 and group_size > 0 and seq_len % group_size == 0)):
+            raise ValueError("group_size must be 0, a multiple of seq_len that divides cols, or a multiple of 16 that divides seq_len")
+        _like(scales, "scales", (cols // group_size if group_size else 1, rows), torch.float32, index)
+    shape = x.shape[:-1] + (rows,)
+    if out is None:
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    else:
+        _like(out, "out", shape, x.dtype, index)
+    _call("bcjr_trellis_matmul", index, x.data_ptr(), kind, x.numel() // cols, rows, cols, packed.data_ptr(),
+          codebook.data_ptr(), _dtype(codebook, "codebook"), state_bits, k, seq_len,
+          None if scales is None else scales.data_ptr(), group_size, out.data_ptr())
+    return out
