@@ -159,8 +159,8 @@ extern "C" bcjr_status bcjr_int4_quantize(const void* w, int w_dtype, int rows, 
                                           bcjr_stream_t stream) {
   if (!dtype_ok(w_dtype) || !dtype_ok(scale_dtype) || rows < 0 || cols < 1 || group_size < 0) return BCJR_ERR_INVALID_ARG;
   if (group_size % 128 != 0 && group_size != 32 && group_size != 64) return BCJR_ERR_UNSUPPORTED;
-  // tiles are the second grid dimension; columns are padded to 128 in ints
-  if (rows > 16 * 65535 || cols > (1 << 30)) return BCJR_ERR_UNSUPPORTED;
+  // tiles are the second grid dimension; columns as in the product
+  if (rows > 16 * 65535 || cols > (1 << 27)) return BCJR_ERR_UNSUPPORTED;
   if (rows == 0) return BCJR_OK;
   if (!w || !packed || !scales || !ptr_aligned(w, dtype_size(w_dtype)) || !ptr_aligned(packed, 16) ||
       !ptr_aligned(scales, dtype_size(scale_dtype)))
