@@ -9,6 +9,7 @@
 // parameter, so a call needs no device memory of its own and no copy.
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "layer_util.cuh"
 
@@ -58,29 +59,42 @@ __host__ __device__ inline void bias_scalars(double lr, double b1, double b2, do
   s.inv_sqrt_bc2 = static_cast<float>(1.0 / sqrt(1.0 - pow(b2, t)));
 }
 
-// 32 bits a (step, seed, element): 16 for either rounding.
-__device__ __forceinline__ uint32_t hash_bits(uint32_t element, uint32_t mix) {
-  uint32_t h = element * 0x9E3779B1u + mix;
+// 32 bits a (step, seed, element), 16 for either rounding: a multiply and
+// xor-shift mix of h = element * kHashA + mix_of(step, seed).
+constexpr uint32_t kHashA = 0x9E3779B1u;
+__device__ __forceinline__ uint32_t hash_bits(uint32_t h) {
   h = (h ^ (h >> 15)) * 0x2C1B3C6Du;
   h = (h ^ (h >> 12)) * 0x297A2D39u;
   return h ^ (h >> 15);
 }
 
-// Magnitude code of t in [0, 448]: scaled by 2^-120 a float's exponent field
-// is e4m3's, so the code is the float's bits cut after three mantissa bits;
-// the 20 bits that fall away decide the rounding together with `rnd`.
-__device__ __forceinline__ uint32_t e4m3_code(float t, uint32_t rnd) {
-  return min((__float_as_uint(__fmul_rn(t, 0x1p-120f)) + rnd) >> 20, 0x7Eu);
-}
+// Magnitude code of x, scaled so that its block's largest is 448 2^-120: a
+// float's exponent field is then e4m3's, so the code is the float's bits cut
+// after three mantissa bits; the 20 bits that fall away decide the rounding
+// together with `rnd`, which is below 2^20 - 4, so that the largest (at most
+// a few places off 448) does not round up.
+__device__ __forceinline__ uint32_t e4m3_code(float x, uint32_t rnd) { return (__float_as_uint(x) + rnd) >> 20; }
 
-__device__ __forceinline__ float e4m3_value(uint32_t byte) {
-  const uint32_t mag = (byte & 0x7Fu) << 20;
-  return __uint_as_float(__float_as_uint(__fmul_rn(__uint_as_float(mag), 0x1p120f)) | ((byte & 0x80u) << 24));
+// Byte i of a word as a float times 2^-120, exactly (subnormal codes are subnormal floats).
+template <bool SIGNED>
+__device__ __forceinline__ float e4m3_small(uint32_t w, int i) {
+  if (SIGNED) return __uint_as_float(static_cast<uint32_t>(static_cast<int32_t>(w << (24 - 8 * i)) >> 4) & 0x87F00000u);
+  return __uint_as_float((i == 3 ? w >> 4 : w << (20 - 8 * i)) & 0x07F00000u);
 }
 
 __device__ __forceinline__ float sqrt_approx(float v) {  // within 2^-23 of the root, denormals included
   float r;
   asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float sqrt_approx_ftz(float v) {  // the same, 0 below 2^-126
+  float r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float v) {  // within 2^-23; 0 above 2^126
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
 
@@ -147,79 +161,130 @@ __device__ __forceinline__ void store8(T* base, int lane, int limit, const T (&v
   }
 }
 
+// m, v and p of one element; r = sqrt(v).  Each product and sum of m and v is
+// rounded on its own, so that a rounding decision of the 8-bit codes does not
+// depend on how the compiler contracts them.
+template <int BITS>
+__device__ __forceinline__ float advance(float& m, float& v, float& r, float g, float p, const Scalars& s) {
+  m = __fadd_rn(__fmul_rn(m, s.b1), __fmul_rn(g, s.c1));
+  v = __fadd_rn(__fmul_rn(v, s.b2), __fmul_rn(__fmul_rn(g, g), s.c2));
+  r = BITS == 32 ? sqrt_approx(v) : sqrt_approx_ftz(v);
+  const float step = m * rcp_approx(fmaf(r, s.inv_sqrt_bc2, s.eps));
+  return fmaf(-s.lr_bc1, step, p * s.decay);
+}
+
 // One block of one tensor.  `limit`: elements of the block that exist.
+template <typename P, typename G, Map MAP>
+__device__ __forceinline__ void block_step32(P* p, const G* g, const Common& c, const Scalars& s, float gs,
+                                             size_t block, int lane, int limit) {
+  float* const first = static_cast<float*>(c.first) + block * kBlock;
+  float* const second = static_cast<float*>(c.second) + block * kBlock;
+  P pv[8];
+  G gv[8];
+  float m[8], v[8];
+  load8<float, MAP>(first, lane, kBlock, m);
+  load8<float, MAP>(second, lane, kBlock, v);
+  load8<G, MAP>(g, lane, limit, gv);
+  load8<P, MAP>(p, lane, limit, pv);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float r;
+    pv[i] = from_f32<P>(advance<32>(m[i], v[i], r, __fmul_rn(to_f32(gv[i]), gs), to_f32(pv[i]), s));
+  }
+  store8<P, MAP>(p, lane, limit, pv);
+  store8<float, MAP>(first, lane, MAP == STRIDED ? limit : kBlock, m);
+  store8<float, MAP>(second, lane, MAP == STRIDED ? limit : kBlock, v);
+}
+
+template <typename P, typename G, Map MAP>
+__device__ __forceinline__ void block_step8(P* p, const G* g, const Common& c, const Scalars& s, float gs,
+                                            size_t block, int lane, int limit) {
+  uint8_t* const first = static_cast<uint8_t*>(c.first) + block * kBlock;
+  uint8_t* const second = static_cast<uint8_t*>(c.second) + block * kBlock;
+  P pv[8];
+  G gv[8];
+  uint8_t a[8], b[8];
+  load8<uint8_t, MAP>(first, lane, kBlock, a);
+  load8<uint8_t, MAP>(second, lane, kBlock, b);
+  load8<G, MAP>(g, lane, limit, gv);
+  load8<P, MAP>(p, lane, limit, pv);
+  const float sa = c.scales[block], sb = c.scales[c.all_blocks + block];
+  uint32_t wa[2], wb[2];
+  memcpy(wa, a, 8);
+  memcpy(wb, b, 8);
+  float m[8], r[8];
+  // A code is its float times 2^-120; bringing that back and the scale are one
+  // product where 2^120 times the scale is a float (a uniform choice: scales
+  // of 128 and more stand for moments beyond 2^15).
+  if (sa < 128.f && sb < 128.f) {
+    const float fa = sa * 0x1p120f, fb = sb * 0x1p120f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      m[i] = __fmul_rn(e4m3_small<true>(wa[i >> 2], i & 3), fa);
+      r[i] = __fmul_rn(e4m3_small<false>(wb[i >> 2], i & 3), fb);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      m[i] = __fmul_rn(__fmul_rn(e4m3_small<true>(wa[i >> 2], i & 3), 0x1p120f), sa);
+      r[i] = __fmul_rn(__fmul_rn(e4m3_small<false>(wb[i >> 2], i & 3), 0x1p120f), sb);
+    }
+  }
+  // the order of the magnitudes' bits is that of the values, NaN above all
+  uint32_t ta = 0, tb = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float v = __fmul_rn(r[i], r[i]);
+    pv[i] = from_f32<P>(advance<8>(m[i], v, r[i], __fmul_rn(to_f32(gv[i]), gs), to_f32(pv[i]), s));
+    if (MAP == STRIDED && element_of<MAP>(lane, i) >= limit) m[i] = r[i] = 0.f;
+    ta = max(ta, __float_as_uint(m[i]) << 1);
+    tb = max(tb, __float_as_uint(r[i]));
+  }
+  store8<P, MAP>(p, lane, limit, pv);
+  const float top_a = __uint_as_float(__reduce_max_sync(~0u, ta) >> 1);
+  const float top_b = __uint_as_float(__reduce_max_sync(~0u, tb) & 0x7FFFFFFFu);
+  const bool held_a = !(top_a < kTiny), held_b = !(top_b < kTiny);
+  float inv_a = held_a ? __fdiv_rn(448.f, top_a) : 0.f, inv_b = held_b ? __fdiv_rn(448.f, top_b) : 0.f;
+  const uint32_t least_b = held_b ? 1u : 0u;  // r > 0 does not become 0
+  // The factor 2^-120 goes into the reciprocal where that stays a normal float.
+  float small = 1.f;
+  if (inv_a >= 0x1p-5f && inv_b >= 0x1p-5f) {
+    inv_a *= 0x1p-120f;
+    inv_b *= 0x1p-120f;
+  } else {
+    small = 0x1p-120f;
+  }
+  uint32_t h0 = (static_cast<uint32_t>(block * kBlock) + element_of<MAP>(lane, 0)) * kHashA + s.mix;
+  auto encode = [&](auto scaled_twice) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t h = hash_bits(h0 + static_cast<uint32_t>(element_of<MAP>(0, i) - element_of<MAP>(0, 0)) * kHashA);
+      float x = __fmul_rn(fabsf(m[i]), inv_a), y = __fmul_rn(r[i], inv_b);
+      if (decltype(scaled_twice)::value) {
+        x = __fmul_rn(x, small);
+        y = __fmul_rn(y, small);
+      }
+      const uint32_t ca = e4m3_code(x, ((h >> 12) & 0xFFFF0u) | 8u);
+      const uint32_t cb = e4m3_code(y, ((h << 4) & 0xFFFF0u) | 8u);
+      a[i] = static_cast<uint8_t>(ca | ((__float_as_uint(m[i]) >> 24) & 0x80u));
+      b[i] = static_cast<uint8_t>(max(cb, min(__float_as_uint(r[i]), least_b)));
+    }
+  };
+  if (small == 1.f) encode(std::false_type{});
+  else encode(std::true_type{});
+  if (lane == 0) {
+    c.scales[block] = held_a ? __fdiv_rn(top_a, 448.f) : 0.f;
+    c.scales[c.all_blocks + block] = held_b ? __fdiv_rn(top_b, 448.f) : 0.f;
+  }
+  store8<uint8_t, MAP>(first, lane, MAP == STRIDED ? limit : kBlock, a);
+  store8<uint8_t, MAP>(second, lane, MAP == STRIDED ? limit : kBlock, b);
+}
+
 template <typename P, typename G, int BITS, Map MAP>
 __device__ __forceinline__ void block_step(P* p, const G* g, const Common& c, const Scalars& s, float gs,
                                            size_t block, int lane, int limit) {
-  using S = typename std::conditional<BITS == 32, float, uint8_t>::type;
-  S* const first = static_cast<S*>(c.first) + block * kBlock;
-  S* const second = static_cast<S*>(c.second) + block * kBlock;
-  P pv[8];
-  G gv[8];
-  S a[8], b[8];
-  load8<S, MAP>(first, lane, kBlock, a);
-  load8<S, MAP>(second, lane, kBlock, b);
-  load8<G, MAP>(g, lane, limit, gv);
-  load8<P, MAP>(p, lane, limit, pv);
-  float sa = 1.f, sb = 1.f;
-  if constexpr (BITS == 8) {
-    sa = c.scales[block];
-    sb = c.scales[c.all_blocks + block];
-  }
-  float m[8], r[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    // each product and sum rounded on its own, so that a rounding decision of
-    // the 8-bit codes does not depend on how the compiler contracts them
-    const float gr = __fmul_rn(to_f32(gv[i]), gs);
-    float v;
-    if constexpr (BITS == 32) {
-      m[i] = a[i];
-      v = b[i];
-    } else {
-      m[i] = __fmul_rn(e4m3_value(a[i]), sa);
-      const float r0 = __fmul_rn(e4m3_value(b[i]), sb);
-      v = __fmul_rn(r0, r0);
-    }
-    m[i] = __fadd_rn(__fmul_rn(m[i], s.b1), __fmul_rn(gr, s.c1));
-    v = __fadd_rn(__fmul_rn(v, s.b2), __fmul_rn(__fmul_rn(gr, gr), s.c2));
-    r[i] = sqrt_approx(v);
-    const float step = __fdividef(m[i], fmaf(r[i], s.inv_sqrt_bc2, s.eps));
-    pv[i] = from_f32<P>(fmaf(-s.lr_bc1, step, to_f32(pv[i]) * s.decay));
-    if constexpr (BITS == 32) {
-      a[i] = m[i];
-      b[i] = v;
-    }
-  }
-  store8<P, MAP>(p, lane, limit, pv);
-  if constexpr (BITS == 8) {
-    // the order of the absolute values' bits is that of the values, NaN above all
-    uint32_t ta = 0, tb = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (MAP == STRIDED && element_of<MAP>(lane, i) >= limit) m[i] = r[i] = 0.f;
-      ta = max(ta, __float_as_uint(m[i]) & 0x7FFFFFFFu);
-      tb = max(tb, __float_as_uint(r[i]) & 0x7FFFFFFFu);
-    }
-    const float top_a = __uint_as_float(__reduce_max_sync(~0u, ta));
-    const float top_b = __uint_as_float(__reduce_max_sync(~0u, tb));
-    const bool held_a = !(top_a < kTiny), held_b = !(top_b < kTiny);
-    const float inv_a = held_a ? __fdiv_rn(448.f, top_a) : 0.f, inv_b = held_b ? __fdiv_rn(448.f, top_b) : 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t h = hash_bits(static_cast<uint32_t>(block * kBlock) + element_of<MAP>(lane, i), s.mix);
-      const uint32_t ca = e4m3_code(__fmul_rn(fabsf(m[i]), inv_a), ((h >> 16) << 4) | 8u);
-      const uint32_t cb = e4m3_code(__fmul_rn(r[i], inv_b), ((h & 0xFFFFu) << 4) | 8u);
-      a[i] = static_cast<uint8_t>(ca | (m[i] < 0.f ? 0x80u : 0u));
-      b[i] = static_cast<uint8_t>(held_b && r[i] > 0.f ? max(cb, 1u) : cb);
-    }
-    if (lane == 0) {
-      c.scales[block] = held_a ? __fdiv_rn(top_a, 448.f) : 0.f;
-      c.scales[c.all_blocks + block] = held_b ? __fdiv_rn(top_b, 448.f) : 0.f;
-    }
-  }
-  store8<S, MAP>(first, lane, MAP == STRIDED ? limit : kBlock, a);
-  store8<S, MAP>(second, lane, MAP == STRIDED ? limit : kBlock, b);
+  if constexpr (BITS == 32) block_step32<P, G, MAP>(p, g, c, s, gs, block, lane, limit);
+  else block_step8<P, G, MAP>(p, g, c, s, gs, block, lane, limit);
 }
 
 template <typename P, typename G, int BITS, int CAP>

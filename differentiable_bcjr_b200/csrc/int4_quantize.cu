@@ -3,11 +3,13 @@
 // A warp takes two rows of a 128-column block at a time: lane l holds columns
 // 8 (l mod 16) .. + 7 of row l / 16, which are the eight codes of one 32-bit
 // word of the packed tile, so a lane reads 16 or 32 contiguous bytes and
-// writes one word.  Groups of 32, 64 and 128 columns are 4, 8 and 16
+// writes one word, four blocks' loads ahead of the work on them.  Groups of 32,
+// 64 and 128 columns are 4, 8 and 16
 // neighbouring lanes, their extremes a few shuffles.  Longer groups take two
 // passes over their blocks, the second from the cache.  Reading w bounds the
 // call (4.5 B a weight for float32 moved in all, 2.5 B for 16-bit types).
 #include <cmath>
+#include <cstring>
 
 #include "layer_util.cuh"
 
@@ -49,70 +51,86 @@ __device__ __forceinline__ void load8(const T* row, int col, int cols, bool fast
   }
 }
 
-// Extremes of a group so far.  Zero is always among the values (lo <= 0 <= hi);
-// a NaN must not be lost, which fminf and fmaxf would do, so it is tracked.
+__device__ __forceinline__ float max_nan(float a, float b) {  // a NaN is not lost, as fmaxf would
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// Extremes of a group so far, with zero among the values: the largest and the
+// largest negated value, or (no zero points) the largest magnitude alone.
+template <bool ZERO>
 struct Extremes {
-  float lo = 0.f, hi = 0.f;
-  bool nan = false;
-  __device__ void add(const float (&v)[8]) {
+  float hi = 0.f, minus_lo = 0.f;
+  __device__ __forceinline__ void add(const float (&v)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      lo = fminf(lo, v[i]);
-      hi = fmaxf(hi, v[i]);
-      nan |= v[i] != v[i];
+      hi = max_nan(hi, ZERO ? v[i] : fabsf(v[i]));
+      if (ZERO) minus_lo = max_nan(minus_lo, -v[i]);
     }
   }
-  __device__ void over(int lanes) {
+  __device__ __forceinline__ void over(int lanes) {
     for (int d = 1; d < lanes; d <<= 1) {
-      lo = fminf(lo, __shfl_xor_sync(~0u, lo, d));
-      hi = fmaxf(hi, __shfl_xor_sync(~0u, hi, d));
-      nan |= __shfl_xor_sync(~0u, static_cast<int>(nan), d) != 0;
+      hi = max_nan(hi, __shfl_xor_sync(~0u, hi, d));
+      if (ZERO) minus_lo = max_nan(minus_lo, __shfl_xor_sync(~0u, minus_lo, d));
     }
   }
 };
 
 struct Code {
-  float inv, zero;
+  float inv;
+  int zero;
 };
 
 // The group's scale (rounded to its type and stored by one lane) and how to
 // take codes with it.  Multiplying by the reciprocal instead of dividing by
 // the scale differs from the quotient's rounding only next to a tie.
-__device__ __forceinline__ Code group_code(const Params& p, const Extremes& e, int row, int group, bool writes) {
-  const float range = p.zeros ? __fsub_rn(e.hi, e.lo) : fmaxf(e.hi, -e.lo);
-  float s = e.nan ? NAN : __fmul_rn(range, p.zeros ? 1.f / 15.f : 1.f / 7.f);
+template <bool ZERO>
+__device__ __forceinline__ Code group_code(const Params& p, const Extremes<ZERO>& e, int row, int group, bool writes) {
+  float s = ZERO ? __fmul_rn(__fadd_rn(e.hi, e.minus_lo), 1.f / 15.f) : __fmul_rn(e.hi, 1.f / 7.f);
   if (p.scale_dtype == BCJR_F16) s = __half2float(__float2half_rn(s));
   else if (p.scale_dtype == BCJR_BF16) s = __bfloat162float(__float2bfloat16_rn(s));
   Code c;
   c.inv = s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
-  c.zero = p.zeros ? fminf(fmaxf(rintf(__fmul_rn(-e.lo, c.inv)), 0.f), 15.f) : 8.f;
+  c.zero = ZERO ? static_cast<int>(fminf(fmaxf(rintf(__fmul_rn(e.minus_lo, c.inv)), 0.f), 15.f)) : 8;
   if (writes && row < p.rows) {
     const size_t i = static_cast<size_t>(group) * p.rows + row;
     store_from_f32(p.scales, p.scale_dtype, i, s);
-    if (p.zeros) p.zeros[i] = static_cast<uint8_t>(c.zero);
+    if (ZERO) p.zeros[i] = static_cast<uint8_t>(c.zero);
   }
   return c;
 }
 
-// Eight columns of a row as the word of the tile that holds them.
+// Eight columns of a row as the word of the tile that holds them.  Adding
+// 1.5 2^23 rounds to the nearest integer, ties to even, and leaves it in the
+// low bits: |w / scale| is at most 30 (a subnormal half scale may be half of
+// what it stands for), and 0 times an infinity, a NaN, takes some code of a
+// group whose scale says so.
 __device__ __forceinline__ void put_word(const Params& p, const float (&v)[8], const Code& c, int tile, int block,
                                          int row16, int l16, bool row_ok, int col) {
   uint32_t word = 0;
 #pragma unroll
   for (int o = 0; o < 8; ++o) {
-    uint32_t q = 8;
-    if (row_ok && col + o < p.cols) {
-      const float f = __fadd_rn(rintf(__fmul_rn(v[o], c.inv)), c.zero);
-      q = static_cast<uint32_t>(fminf(fmaxf(f, 0.f), 15.f));  // a NaN gives 0
-    }
+    const int rounded = __float_as_int(__fadd_rn(__fmul_rn(v[o], c.inv), 12582912.f)) - 0x4B400000;
+    const uint32_t q = static_cast<uint32_t>(min(max(rounded + c.zero, 0), 15));
     word |= q << (4 * (o >> 1) + 16 * (o & 1));
+  }
+  if (!row_ok) word = 0x88888888u;
+  else if (col + 8 > p.cols) {
+#pragma unroll
+    for (int o = 0; o < 8; ++o) {
+      const int at = 4 * (o >> 1) + 16 * (o & 1);
+      if (col + o >= p.cols) word = (word & ~(15u << at)) | (8u << at);
+    }
   }
   const size_t at = (static_cast<size_t>(tile) * p.blocks + block) * 1024 + (row16 >> 3) * 512 + (row16 & 7) * 64 +
                     (l16 & 3) * 16 + (l16 >> 2) * 4;
   *reinterpret_cast<uint32_t*>(p.packed + at) = word;
 }
 
-template <typename T>
+constexpr int kAtOnce = 4;  // blocks that a thread loads before it works on them
+
+template <typename T, bool ZERO>
 __global__ void __launch_bounds__(kWarps * 32) int4_quantize_kernel(const __grid_constant__ Params p) {
   const int lane = threadIdx.x & 31, l16 = lane & 15;
   const int row16 = (threadIdx.x >> 5) * 2 + (lane >> 4);
@@ -121,35 +139,49 @@ __global__ void __launch_bounds__(kWarps * 32) int4_quantize_kernel(const __grid
   const bool ok = row < p.rows;
   const T* const src = static_cast<const T*>(p.w) + static_cast<size_t>(ok ? row : p.rows - 1) * p.cols;
   const bool fast = (p.cols * sizeof(T)) % 16 == 0 && (reinterpret_cast<uintptr_t>(p.w) & 15) == 0;
-  float v[8];
   if (p.group_blocks == 0) {
-    for (int block = blockIdx.x; block < p.blocks; block += gridDim.x) {
-      const int col = block * 128 + l16 * 8;
-      load8(src, col, p.cols, fast, v);
-      Extremes e;
-      e.add(v);
+    const int b0 = blockIdx.x * kAtOnce;
+    float v[kAtOnce][8];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) load8(src, (b0 + i) * 128 + l16 * 8, p.cols, fast, v[i]);
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int block = b0 + i, col = block * 128 + l16 * 8;
+      if (block >= p.blocks) break;
+      Extremes<ZERO> e;
+      e.add(v[i]);
       e.over(p.lanes);
       const int group = block * (16 / p.lanes) + l16 / p.lanes;
       const Code c = group_code(p, e, row, group, l16 % p.lanes == 0 && group < p.groups);
-      put_word(p, v, c, tile, block, row16, l16, ok, col);
+      put_word(p, v[i], c, tile, block, row16, l16, ok, col);
     }
   } else {
-    for (int group = blockIdx.x; group < p.groups; group += gridDim.x) {
-      const int b0 = group * p.group_blocks, b1 = min(b0 + p.group_blocks, p.blocks);
-      Extremes e;
-      for (int block = b0; block < b1; ++block) {
-        load8(src, block * 128 + l16 * 8, p.cols, fast, v);
-        e.add(v);
-      }
-      e.over(16);
-      const Code c = group_code(p, e, row, group, l16 == 0);
-      for (int block = b0; block < b1; ++block) {
-        const int col = block * 128 + l16 * 8;
-        load8(src, col, p.cols, fast, v);
-        put_word(p, v, c, tile, block, row16, l16, ok, col);
-      }
+    const int group = blockIdx.x;
+    const int b0 = group * p.group_blocks, b1 = min(b0 + p.group_blocks, p.blocks);
+    float v[8];
+    Extremes<ZERO> e;
+#pragma unroll 4
+    for (int block = b0; block < b1; ++block) {
+      load8(src, block * 128 + l16 * 8, p.cols, fast, v);
+      e.add(v);
+    }
+    e.over(16);
+    const Code c = group_code(p, e, row, group, l16 == 0);
+#pragma unroll 4
+    for (int block = b0; block < b1; ++block) {
+      const int col = block * 128 + l16 * 8;
+      load8(src, col, p.cols, fast, v);
+      put_word(p, v, c, tile, block, row16, l16, ok, col);
     }
   }
+}
+
+template <typename T>
+void launch(const Params& p, cudaStream_t s) {
+  const int units = p.group_blocks ? p.groups : (p.blocks + kAtOnce - 1) / kAtOnce;
+  const dim3 grid(static_cast<unsigned>(units), static_cast<unsigned>((p.rows + 15) / 16));
+  if (p.zeros) int4_quantize_kernel<T, true><<<grid, kWarps * 32, 0, s>>>(p);
+  else int4_quantize_kernel<T, false><<<grid, kWarps * 32, 0, s>>>(p);
 }
 
 }  // namespace
@@ -185,11 +217,9 @@ extern "C" bcjr_status bcjr_int4_quantize(const void* w, int w_dtype, int rows, 
     p.group_blocks = group_size / 128;
     p.groups = (cols + group_size - 1) / group_size;
   }
-  const int units = p.group_blocks ? p.groups : p.blocks;
-  const dim3 grid(static_cast<unsigned>(units), static_cast<unsigned>((rows + 15) / 16));
   cudaStream_t s = as_stream(stream);
-  if (w_dtype == BCJR_F32) int4_quantize_kernel<float><<<grid, kWarps * 32, 0, s>>>(p);
-  else if (w_dtype == BCJR_F16) int4_quantize_kernel<__half><<<grid, kWarps * 32, 0, s>>>(p);
-  else int4_quantize_kernel<__nv_bfloat16><<<grid, kWarps * 32, 0, s>>>(p);
+  if (w_dtype == BCJR_F32) launch<float>(p, s);
+  else if (w_dtype == BCJR_F16) launch<__half>(p, s);
+  else launch<__nv_bfloat16>(p, s);
   return launched();
 }

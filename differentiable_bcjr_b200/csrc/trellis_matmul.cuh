@@ -1,0 +1,285 @@
+// trellis_matmul.cuh -- a few tokens times packed trellis weights (bcjr_trellis_matmul).
+//
+// A weight is codebook[state], and a step's state is a window of the packed
+// stream, so the weights of a chunk of CH steps come out of two or three
+// words by funnel shifts.  The codebook sits in shared memory; its random
+// gathers bound the call: 32 lanes hit 32 banks at random, about 3.5 clocks a
+// warp, where the packed words themselves are k bits a weight.  Small
+// codebooks are kept in several copies, lane l reading copy l mod copies, so
+// that lanes of different copies never meet in a bank.
+//
+// A lane keeps the inputs of its chunk of columns in registers and walks down
+// the rows, the next rows' words on their way; a row's sums are added over the
+// warp with a transposing butterfly (eight sums in nine shuffles) and over the
+// warps in a fixed order.
+//
+// Codebooks up to 2^15 states are held in float32 (other types convert
+// exactly), 2^16 states of a 16-bit type as they are (128 KiB), and 2^16
+// float32 states in two halves, one after the other: the rows are walked
+// twice, every state's gather being skipped in the walk that lacks it (half
+// the lanes of a gather meet in fewer banks, so both walks together take less
+// than two full ones).
+#pragma once
+#include <type_traits>
+
+#include "layer_util.cuh"
+#include "trellis_internal.h"
+
+namespace bcjr {
+namespace {
+
+using Params = TrellisMatmulParams;
+
+constexpr int kWarps = 16;
+constexpr int kSums = 512;  // row sums a warp can hold in shared memory
+
+enum Held { F32, B16, H16, HALVES };
+
+// The sums over the warp of eight values a lane: lane l gets in v[0] that of value l >> 2.
+__device__ __forceinline__ void sum8(float (&v)[8], int lane) {
+#pragma unroll
+  for (int step = 0; step < 3; ++step) {
+    const int half = 4 >> step, d = 16 >> step;
+    const bool upper = (lane & d) != 0;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float give = upper ? v[i] : v[i + half], keep = upper ? v[i + half] : v[i];
+      v[i] = keep + __shfl_xor_sync(~0u, give, d);
+    }
+  }
+  v[0] += __shfl_xor_sync(~0u, v[0], 2);
+  v[0] += __shfl_xor_sync(~0u, v[0], 1);
+}
+
+// bits [at, at + 32) of a stream's words
+template <int N>
+__device__ __forceinline__ uint32_t shifted(const uint32_t (&a)[N], int at) {
+  return at % 32 == 0 ? a[at / 32] : __funnelshift_l(a[at / 32 + 1], a[at / 32], at % 32);
+}
+
+// The codeword of the state whose first bit is bit `at` of the chunk; false:
+// it is in the other half of the codebook.
+template <Held HELD, int N>
+__device__ __forceinline__ bool codeword(const unsigned char* table, uint32_t lane_copy, int shift, uint32_t mask,
+                                         uint32_t phase_bit, const uint32_t (&a)[N], int at, float& c) {
+  if constexpr (HELD == F32) {
+    // shift and mask leave the state times the bytes between its copies
+    const uint32_t offset = ((shifted(a, at) >> shift) & mask) | lane_copy;
+    c = *reinterpret_cast<const float*>(table + offset);
+    return true;
+  } else {
+    // 16 bits a state: constant shifts put it above the byte offset's low bits
+    constexpr int LOW = HELD == HALVES ? 2 : 1;
+    const int down = 48 - at % 32 - LOW;
+    const uint32_t q = down >= 32 ? a[at / 32] >> (down - 32) : __funnelshift_r(a[at / 32 + 1], a[at / 32], down);
+    if constexpr (HELD == HALVES) {
+      if ((q & 0x20000u) != phase_bit) return false;
+      c = *reinterpret_cast<const float*>(table + (q & 0x1FFFCu));
+    } else if constexpr (HELD == B16) {
+      c = __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(table + (q & 0x1FFFEu))) << 16);
+    } else {
+      c = __half2float(*reinterpret_cast<const __half*>(table + (q & 0x1FFFEu)));
+    }
+    return true;
+  }
+}
+
+// `bytes` (a multiple of 16) into shared memory, 16 at a time where the source allows.
+__device__ __forceinline__ void copy_in(unsigned char* to, const unsigned char* from, int bytes) {
+  if ((reinterpret_cast<uintptr_t>(from) & 15) == 0) {
+#pragma unroll 8
+    for (int i = threadIdx.x; i < bytes / 16; i += kWarps * 32) reinterpret_cast<uint4*>(to)[i] = reinterpret_cast<const uint4*>(from)[i];
+  } else {
+    for (int i = threadIdx.x; i < bytes / 2; i += kWarps * 32) reinterpret_cast<uint16_t*>(to)[i] = reinterpret_cast<const uint16_t*>(from)[i];
+  }
+}
+
+template <int K, int MT, int CH, Held HELD>
+__global__ void __launch_bounds__(kWarps * 32, 1) trellis_matmul_kernel(const __grid_constant__ Params p) {
+  constexpr int ROWS = 8 / MT;  // rows whose sums are added over the warp together
+  // a chunk starts at a multiple of CH K bits, so at worst at this bit of a word
+  constexpr int STEP = (CH * K) % 32 == 0 ? 32 : (CH * K) % 16 == 0 ? 16 : 8;
+  constexpr int WORDS = (32 - STEP + (CH - 1) * K + 16 + 31) / 32;
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = 1 << p.L;
+  const size_t table_bytes = HELD == F32 ? static_cast<size_t>(S) * 4 << p.copies_log2 : static_cast<size_t>(S) * 2;
+  float* const sums = reinterpret_cast<float*>(smem + (table_bytes + 15) / 16 * 16) + warp * kSums;  // of [kWarps][kSums]
+  const uint32_t lane_copy = (lane & ((1u << p.copies_log2) - 1u)) * 4;
+  const int shift = 30 - p.L - p.copies_log2;
+  const uint32_t mask = (static_cast<uint32_t>(S) - 1u) << (2 + p.copies_log2);
+
+  const int tiles = (p.chunks + 31) / 32;
+  const int teams = kWarps / p.wide;  // rows walked side by side
+  const int team = warp / p.wide, place = warp % p.wide;
+  const int r_begin = static_cast<int>(static_cast<long long>(p.rows) * blockIdx.x / gridDim.x);
+  const int r_end = static_cast<int>(static_cast<long long>(p.rows) * (blockIdx.x + 1) / gridDim.x);
+  constexpr int ROOM = kSums / MT;  // rows a team can hold sums of
+  const int token0 = blockIdx.y * MT;
+  const int tokens = min(MT, p.tokens - token0);
+
+  constexpr int PHASES = HELD == HALVES ? 2 : 1;
+  for (int r0 = r_begin; r0 < r_end; r0 += ROOM * teams) {
+    const int r1 = min(r0 + ROOM * teams, r_end);
+    for (int i = lane; i < kSums; i += 32) sums[i] = 0.f;
+    __syncwarp();
+    for (int phase = 0; phase < PHASES; ++phase) {
+      if (HELD == HALVES || r0 == r_begin) {
+        if (HELD == HALVES) __syncthreads();  // the last half's readers are done
+        if constexpr (HELD == F32) {
+#pragma unroll 8
+          for (int i = threadIdx.x; i < (S << p.copies_log2); i += kWarps * 32)
+            reinterpret_cast<float*>(smem)[i] = load_as_f32(p.codebook, p.c_dtype, i >> p.copies_log2);
+        } else {
+          copy_in(smem, static_cast<const unsigned char*>(p.codebook) + phase * 131072, 131072);
+        }
+        __syncthreads();
+      }
+      const uint32_t phase_bit = phase ? 0x20000u : 0u;
+      for (int tile = place; tile < tiles; tile += p.wide) {
+        const int q = tile * 32 + lane;
+        const bool have = q < p.chunks;
+        const int seq = (have ? q : 0) / p.per_seq;
+        const int t0 = ((have ? q : 0) - seq * p.per_seq) * CH;
+        const int count = min(CH, p.n - t0);
+        const int col = seq * p.n + t0;
+        float x[CH][MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const size_t at = static_cast<size_t>(token0 + min(m, tokens - 1)) * p.cols + col;
+#pragma unroll
+          for (int i = 0; i < CH; ++i) x[i][m] = i < count ? load_as_f32(p.x, p.x_dtype, at + i) : 0.f;
+        }
+        const int bit = t0 * K, skew = bit & 31;
+        const uint32_t* const stream = p.packed + static_cast<size_t>(seq) * p.words;
+        int word[WORDS];  // a chunk at the sequence's end may have fewer words left
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) word[i] = min((bit >> 5) + i, p.words - 1);
+        const size_t row_words = static_cast<size_t>(p.seqs) * p.words;
+        const float* const scale = p.scales ? p.scales + static_cast<size_t>(col / p.group) * p.rows : nullptr;
+
+        auto walk = [&](auto whole) {
+          constexpr bool WHOLE = decltype(whole)::value;  // every lane's chunk has all CH steps
+          uint32_t next[ROWS][WORDS];
+          float next_scale[ROWS];
+          auto fetch = [&](int rb) {
+#pragma unroll
+            for (int rr = 0; rr < ROWS; ++rr) {
+              if (rb + rr >= r1) break;
+              const uint32_t* const from = stream + (rb + rr) * row_words;
+#pragma unroll
+              for (int i = 0; i < WORDS; ++i) next[rr][i] = __ldg(from + word[i]);
+              next_scale[rr] = scale ? __ldg(scale + rb + rr) : 1.f;
+            }
+          };
+          fetch(r0 + team * ROWS);
+          for (int rb = r0 + team * ROWS; rb < r1; rb += teams * ROWS) {
+            uint32_t now[ROWS][WORDS];
+            float now_scale[ROWS];
+#pragma unroll
+            for (int rr = 0; rr < ROWS; ++rr) {
+#pragma unroll
+              for (int i = 0; i < WORDS; ++i) now[rr][i] = next[rr][i];
+              now_scale[rr] = next_scale[rr];
+            }
+            fetch(rb + teams * ROWS);
+            float v[8];
+#pragma unroll
+            for (int rr = 0; rr < ROWS; ++rr) {
+              if (rb + rr >= r1) {
+#pragma unroll
+                for (int m = 0; m < MT; ++m) v[rr * MT + m] = 0.f;
+                continue;
+              }
+              uint32_t a[WORDS + 1];
+#pragma unroll
+              for (int i = 0; i < WORDS; ++i) a[i] = now[rr][i];
+              a[WORDS] = 0;
+              if constexpr (STEP != 32) {
+#pragma unroll
+                for (int i = 0; i < WORDS; ++i) a[i] = __funnelshift_l(a[i + 1], a[i], skew);
+              }
+              float acc[MT] = {};
+#pragma unroll
+              for (int i = 0; i < CH; ++i) {
+                float c;
+                bool add = codeword<HELD>(smem, lane_copy, shift, mask, phase_bit, a, i * K, c);
+                if (!WHOLE) add = add && i < count;
+                // (a product with 0 would not do: the codeword or the input may be infinite)
+                if (add) {
+#pragma unroll
+                  for (int m = 0; m < MT; ++m) acc[m] = fmaf(c, x[i][m], acc[m]);
+                }
+              }
+#pragma unroll
+              for (int m = 0; m < MT; ++m) v[rr * MT + m] = have ? acc[m] * now_scale[rr] : 0.f;
+            }
+            sum8(v, lane);
+            if ((lane & 3) == 0) {
+              const int i = lane >> 2, rr = i / MT, m = i % MT;
+              if (rb + rr < r1) sums[((rb - r0) / (teams * ROWS) * ROWS + rr) * MT + m] += v[0];
+            }
+            __syncwarp();
+          }
+        };
+        if (__all_sync(~0u, count == CH)) walk(std::true_type{});
+        else walk(std::false_type{});
+      }
+    }
+    __syncthreads();
+    const float* const all = sums - warp * kSums;
+    for (int i = threadIdx.x; i < (r1 - r0) * tokens; i += kWarps * 32) {
+      const int row = i % (r1 - r0), m = i / (r1 - r0);
+      const int turn = row / (teams * ROWS), of = row % (teams * ROWS);
+      const float* const from = all + (of / ROWS * p.wide) * kSums + (turn * ROWS + of % ROWS) * MT + m;
+      float v = 0.f;
+      for (int w = 0; w < p.wide; ++w) v += from[w * kSums];
+      store_from_f32(p.y, p.x_dtype, static_cast<size_t>(token0 + m) * p.rows + r0 + row, v);
+    }
+    __syncthreads();
+  }
+}
+
+template <int K, int MT, int CH, Held HELD>
+bcjr_status launch(Params p, int sms, cudaStream_t s) {
+  p.per_seq = (p.n + CH - 1) / CH;
+  p.chunks = p.seqs * p.per_seq;
+  const int tiles = (p.chunks + 31) / 32;
+  p.wide = 1;
+  while (p.wide < kWarps && p.wide < tiles) p.wide *= 2;
+  const size_t S = size_t{1} << p.L;
+  p.copies_log2 = 0;
+  if (HELD == F32) {
+    while (p.copies_log2 < 5 && (S * 4 << (p.copies_log2 + 1)) <= (128u << 10)) ++p.copies_log2;
+  }
+  const size_t table = HELD == F32 ? S * 4 << p.copies_log2 : S * 2;
+  const size_t smem = (table + 15) / 16 * 16 + sizeof(float) * kWarps * kSums;
+  auto* const kernel = trellis_matmul_kernel<K, MT, CH, HELD>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) {
+    cudaGetLastError();
+    return BCJR_ERR_CUDA;
+  }
+  const int teams = kWarps / p.wide;
+  const int most = (p.rows + teams - 1) / teams;
+  const dim3 grid(static_cast<unsigned>(most < sms ? most : sms), static_cast<unsigned>((p.tokens + MT - 1) / MT));
+  kernel<<<grid, kWarps * 32, smem, s>>>(p);
+  return launched();
+}
+
+template <int K, Held HELD>
+bcjr_status launch_tokens(const Params& p, int sms, cudaStream_t s) {
+  if (p.tokens == 1) return launch<K, 1, 16, HELD>(p, sms, s);
+  if (p.tokens <= 4) return launch<K, 4, 16, HELD>(p, sms, s);
+  return launch<K, 8, 8, HELD>(p, sms, s);
+}
+
+template <int K>
+bcjr_status launch_held(const Params& p, int sms, cudaStream_t s) {
+  if (p.L < 16) return launch_tokens<K, F32>(p, sms, s);
+  if (p.c_dtype == BCJR_F32) return launch_tokens<K, HALVES>(p, sms, s);
+  if (p.c_dtype == BCJR_BF16) return launch_tokens<K, B16>(p, sms, s);
+  return launch_tokens<K, H16>(p, sms, s);
+}
+
+}  // namespace
+}  // namespace bcjr

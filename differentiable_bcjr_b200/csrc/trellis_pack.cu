@@ -1,52 +1,105 @@
 // trellis_pack.cu -- hard-decoded states to k bits a weight (bcjr_trellis_pack).
 //
-// A thread writes one 32-bit word of a sequence's stream from the low k bits
-// of the 8 to 33 states that begin or end in it.  Reading the states (4 B a
-// weight) bounds the call.
+// The stream of a sequence is the state_bits - k upper bits of its first state
+// and then the low k bits of every state.  A warp takes 32 pieces of 32 states:
+// it loads them piece by piece, coalesced, leaves the low bits as bytes in
+// shared memory, and then lane l puts the words of piece l together.  What
+// precedes a piece in the stream are the upper bits of its first state, so no
+// piece waits for another.  Reading the states (4 B a weight) bounds the call.
 #include "layer_util.cuh"
 
 namespace {
 
 using namespace bcjr;
 
+constexpr int kWarps = 8;
+constexpr int kPitch = 36;  // bytes of a piece's codes in shared memory: lanes read theirs from different banks
+
 struct Params {
   const int32_t* states;
   uint32_t* packed;
   int* bad;
   int L, n, words;
-  long long total;  // words of all sequences
+  int per_seq;      // pieces of a sequence
+  long long total;  // pieces of all sequences
 };
 
-template <int K>
-__global__ void __launch_bounds__(256) trellis_pack_kernel(const __grid_constant__ Params p) {
-  const long long id = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-  if (id >= p.total) return;
-  const long long seq = id / p.words;
-  const int j = static_cast<int>(id - seq * p.words);
-  const int32_t* const s = p.states + seq * p.n;
-  // Step t ends at bit t K + L of the stream; the steps that end behind the
-  // word's first bit and do not begin behind its last are those that touch it
-  // with their last K bits (or, the first step, with any).
-  const int begin = 32 * j;
-  uint32_t word = 0;
+template <int K, bool CHECK>
+__global__ void __launch_bounds__(kWarps * 32) trellis_pack_kernel(const __grid_constant__ Params p) {
+  __shared__ __align__(4) uint8_t codes[kWarps][32 * kPitch];
+  const int lane = threadIdx.x & 31;
+  uint8_t* const mine = codes[threadIdx.x >> 5];
+  const long long q0 = (static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * 32;
+  if (q0 >= p.total) return;
+  long long seq = q0 / p.per_seq;
+  int piece = static_cast<int>(q0 - seq * p.per_seq);
+  // lane l's own piece
+  const long long q = q0 + lane;
+  const long long my_seq = q / p.per_seq;
+  const int my_piece = static_cast<int>(q - my_seq * p.per_seq);
+  const bool have = q < p.total;
+  const uint32_t my_first = have ? static_cast<uint32_t>(p.states[my_seq * p.n + 32 * my_piece]) : 0u;
+
   bool bad = false;
-  int t = (begin - p.L) / K + 1;  // the first step that ends behind `begin`
-  if (begin < p.L) t = 0;
-  uint32_t before = t > 0 ? static_cast<uint32_t>(s[t - 1]) : 0u;
-  for (; t < p.n; ++t) {
-    const int end = t * K + p.L;  // relative to the stream
-    const int bits = t == 0 ? p.L : K;
-    if (end - bits >= begin + 32) break;
-    const uint32_t state = static_cast<uint32_t>(s[t]);
-    const uint32_t mask = (1u << p.L) - 1u;
-    bad |= (state & ~mask) != 0u || (t > 0 && (state >> K) != (before & (mask >> K)));
-    before = state;
-    const uint32_t v = state & ((1u << bits) - 1u);
-    const int up = begin + 32 - end;  // places below the word's last bit
-    word |= up >= 0 ? v << up : v >> -up;
+#pragma unroll 8
+  for (int i = 0; i < 32; ++i) {
+    uint32_t state = 0;
+    if (q0 + i < p.total) {
+      const int t = 32 * piece + lane;
+      const int32_t* const at = p.states + seq * p.n + t;
+      if (t < p.n) state = static_cast<uint32_t>(*at);
+      if constexpr (CHECK) {
+        const uint32_t mask = (1u << p.L) - 1u;
+        uint32_t before = __shfl_up_sync(~0u, state, 1);
+        if (lane == 0 && t > 0) before = static_cast<uint32_t>(at[-1]);
+        if (t < p.n) bad |= (state & ~mask) != 0u || (t > 0 && (state >> K) != (before & (mask >> K)));
+      }
+    }
+    mine[i * kPitch + lane] = static_cast<uint8_t>(state & ((1u << K) - 1u));
+    if (++piece == p.per_seq) {
+      piece = 0;
+      ++seq;
+    }
   }
-  p.packed[id] = word;
-  if (bad && p.bad) *p.bad = 1;
+  if (CHECK && bad) *p.bad = 1;
+  __syncwarp();
+  if (!have) return;
+
+  uint32_t body[K + 1];  // 32 K bits, the first state's highest; then none
+#pragma unroll
+  for (int w = 0; w <= K; ++w) body[w] = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    const uint32_t four = *reinterpret_cast<const uint32_t*>(mine + lane * kPitch + 4 * w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t c = (four >> (8 * i)) & ((1u << K) - 1u);
+      const int bit = (4 * w + i) * K, up = 32 - K - bit % 32;  // places below the word's last bit
+      if (up >= 0) {
+        body[bit / 32] |= c << up;
+      } else {
+        body[bit / 32] |= c >> -up;
+        body[bit / 32 + 1] |= c << (32 + up);
+      }
+    }
+  }
+  const int o = p.L - K;  // bits before the piece that belong to its first word
+  uint32_t* const out = p.packed + my_seq * p.words;
+  uint32_t before = my_first >> K;
+#pragma unroll
+  for (int w = 0; w <= K; ++w) {
+    // the word after the last piece's holds the bits that are left over
+    const int j = K * my_piece + w;
+    if (j < p.words && (w < K || my_piece == p.per_seq - 1)) out[j] = __funnelshift_r(body[w], before, o);
+    before = body[w];
+  }
+}
+
+template <int K>
+bcjr_status launch(const Params& p, unsigned grid, cudaStream_t s) {
+  if (p.bad) trellis_pack_kernel<K, true><<<grid, kWarps * 32, 0, s>>>(p);
+  else trellis_pack_kernel<K, false><<<grid, kWarps * 32, 0, s>>>(p);
+  return launched();
 }
 
 }  // namespace
@@ -66,15 +119,15 @@ extern "C" bcjr_status bcjr_trellis_pack(const int32_t* states, int state_bits, 
   p.L = state_bits;
   p.n = seq_len;
   p.words = static_cast<int>((static_cast<long long>(seq_len) * k + state_bits - k + 31) / 32);
-  p.total = static_cast<long long>(p.words) * n_seq;
-  const long long grid = (p.total + 255) / 256;
+  p.per_seq = (seq_len + 31) / 32;
+  p.total = static_cast<long long>(p.per_seq) * n_seq;
+  const long long grid = (p.total + 32 * kWarps - 1) / (32 * kWarps);
   if (grid > 0x7FFFFFFFll) return BCJR_ERR_UNSUPPORTED;
   cudaStream_t s = as_stream(stream);
   switch (k) {
-    case 1: trellis_pack_kernel<1><<<static_cast<unsigned>(grid), 256, 0, s>>>(p); break;
-    case 2: trellis_pack_kernel<2><<<static_cast<unsigned>(grid), 256, 0, s>>>(p); break;
-    case 3: trellis_pack_kernel<3><<<static_cast<unsigned>(grid), 256, 0, s>>>(p); break;
-    default: trellis_pack_kernel<4><<<static_cast<unsigned>(grid), 256, 0, s>>>(p); break;
+    case 1: return launch<1>(p, static_cast<unsigned>(grid), s);
+    case 2: return launch<2>(p, static_cast<unsigned>(grid), s);
+    case 3: return launch<3>(p, static_cast<unsigned>(grid), s);
+    default: return launch<4>(p, static_cast<unsigned>(grid), s);
   }
-  return launched();
 }

@@ -239,8 +239,8 @@ def trellis_pack(states, state_bits, k, check=False):
     """Hard-decoded states (int32 [n_seq][seq_len], as `viterbi_decode` gives
     them) as one bit stream a sequence, k bits a step after the first:
     int32 [n_seq][trellis_words(state_bits, k, seq_len)].  With `check` the
-    call waits for the GPU and raises if some state does not follow from the
-    one before; without it such a state's upper bits are lost."""
+    call waits for the GPU and raises if the states are no path of the trellis;
+    without it the words of such a sequence mean nothing."""
     index = _on_device(states, "states")
     if states.dim() != 2 or states.shape[1] < 1 or states.dtype != torch.int32:
         raise ValueError("states must be int32 [n_seq][seq_len]")

@@ -112,10 +112,10 @@ bcjr_status bcjr_int4_matmul(const void* x, int x_dtype, int tokens, int rows, i
  * state_bits bits for the first step and k for every other.  Bits behind the
  * end are zero.  1 <= k <= 4, k <= state_bits <= 16.
  *
- * bcjr_trellis_pack packs states [n_seq][seq_len] (int32).  Of a step after
- * the first only the low k bits are read into the stream; when `bad` (device,
- * one int) is given, it is set to 1 if some step does not follow from the one
- * before or a state is out of range, and left as it is otherwise.
+ * bcjr_trellis_pack packs states [n_seq][seq_len] (int32), which must be paths
+ * of the trellis: when `bad` (device, one int) is given, it is set to 1 if some
+ * step does not follow from the one before or a state is out of range, and left
+ * as it is otherwise; the words of such a sequence are then not a path's.
  */
 bcjr_status bcjr_trellis_pack(const int32_t* states, int state_bits, int k, int seq_len, int n_seq,
                               uint32_t* packed, int* bad, bcjr_stream_t stream);
