@@ -7,8 +7,11 @@
 // scales belong to; a warp takes one block at a time, 8 elements a lane, and
 // finds its tensor by bisection in a table that travels as a kernel
 // parameter, so a call needs no device memory of its own and no copy.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <memory>
+#include <new>
 #include <type_traits>
 
 #include "layer_util.cuh"
@@ -35,6 +38,7 @@ struct Table {
   int first_block[CAP];  // relative to the launch's first block
   int n;
   int blocks;            // of the launch
+  int each;              // blocks of a warp
 };
 
 struct Common {
@@ -244,7 +248,7 @@ __device__ __forceinline__ void block_step8(P* p, const G* g, const Common& c, c
   const float top_a = __uint_as_float(__reduce_max_sync(~0u, ta) >> 1);
   const float top_b = __uint_as_float(__reduce_max_sync(~0u, tb) & 0x7FFFFFFFu);
   const bool held_a = !(top_a < kTiny), held_b = !(top_b < kTiny);
-  float inv_a = held_a ? __fdiv_rn(448.f, top_a) : 0.f, inv_b = held_b ? __fdiv_rn(448.f, top_b) : 0.f;
+  float inv_a = held_a ? __fmul_rn(rcp_approx(top_a), 448.f) : 0.f, inv_b = held_b ? __fmul_rn(rcp_approx(top_b), 448.f) : 0.f;
   const uint32_t least_b = held_b ? 1u : 0u;  // r > 0 does not become 0
   // The factor 2^-120 goes into the reciprocal where that stays a normal float.
   float small = 1.f;
@@ -273,8 +277,8 @@ __device__ __forceinline__ void block_step8(P* p, const G* g, const Common& c, c
   if (small == 1.f) encode(std::false_type{});
   else encode(std::true_type{});
   if (lane == 0) {
-    c.scales[block] = held_a ? __fdiv_rn(top_a, 448.f) : 0.f;
-    c.scales[c.all_blocks + block] = held_b ? __fdiv_rn(top_b, 448.f) : 0.f;
+    c.scales[block] = held_a ? __fmul_rn(top_a, 1.f / 448.f) : 0.f;
+    c.scales[c.all_blocks + block] = held_b ? __fmul_rn(top_b, 1.f / 448.f) : 0.f;
   }
   store8<uint8_t, MAP>(first, lane, MAP == STRIDED ? limit : kBlock, a);
   store8<uint8_t, MAP>(second, lane, MAP == STRIDED ? limit : kBlock, b);
@@ -304,29 +308,35 @@ __global__ void __launch_bounds__(kWarps * 32) adamw_kernel(const __grid_constan
   }
   const float gs = c.grad_scale ? *c.grad_scale : 1.f;
   const int lane = threadIdx.x & 31;
-  const int b = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (b >= t.blocks) return;
+  int b = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * t.each;
+  const int end = min(b + t.each, t.blocks);
+  if (b >= end) return;
   int lo = 0, hi = t.n - 1;  // the last tensor that starts at or before b
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (t.first_block[mid] <= b) lo = mid;
     else hi = mid - 1;
   }
-  if (!t.g[lo]) return;
-  const int64_t at = static_cast<int64_t>(b - t.first_block[lo]) * kBlock;
-  const int64_t left = t.numel[lo] - at;
-  P* const p = static_cast<P*>(t.p[lo]) + at;
-  const G* const g = static_cast<const G*>(t.g[lo]) + at;
-  const size_t block = c.block0 + b;
   constexpr Map FULL = (BITS == 8 && sizeof(P) == 2 && sizeof(G) == 2) ? PACKED : COALESCED;
-  if (left >= kBlock && ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(g)) & 15) == 0)
-    block_step<P, G, BITS, FULL>(p, g, c, s, gs, block, lane, kBlock);
-  else
-    block_step<P, G, BITS, STRIDED>(p, g, c, s, gs, block, lane, left < kBlock ? static_cast<int>(left) : kBlock);
+  for (; b < end; ++b) {
+    while (lo + 1 < t.n && t.first_block[lo + 1] <= b) ++lo;
+    if (!t.g[lo]) continue;
+    const int64_t at = static_cast<int64_t>(b - t.first_block[lo]) * kBlock;
+    const int64_t left = t.numel[lo] - at;
+    P* const p = static_cast<P*>(t.p[lo]) + at;
+    const G* const g = static_cast<const G*>(t.g[lo]) + at;
+    const size_t block = c.block0 + b;
+    if (left >= kBlock && ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(g)) & 15) == 0)
+      block_step<P, G, BITS, FULL>(p, g, c, s, gs, block, lane, kBlock);
+    else
+      block_step<P, G, BITS, STRIDED>(p, g, c, s, gs, block, lane, left < kBlock ? static_cast<int>(left) : kBlock);
+  }
 }
 
 template <typename P, typename G, int BITS, int CAP>
 bcjr_status launch(const bcjr_adamw_tensor* ts, int n, Common& c, cudaStream_t stream) {
+  const int sms = sm_count();
+  if (sms <= 0) return BCJR_ERR_CUDA;
   Table<CAP> t;
   t.n = 0;
   int64_t blocks = 0;
@@ -335,7 +345,11 @@ bcjr_status launch(const bcjr_adamw_tensor* ts, int n, Common& c, cudaStream_t s
     // a launch's blocks are counted in an int
     if (t.n > 0 && (i == n || t.n == CAP || blocks + more > (int64_t{1} << 30))) {
       t.blocks = static_cast<int>(blocks);
-      const unsigned grid = static_cast<unsigned>((blocks + kWarps - 1) / kWarps);
+      // finding a block's tensor and the step's constants costs as much as some
+      // elements do: several blocks a warp once there are enough for all warps
+      t.each = BITS == 8 && blocks >= int64_t{4} * 64 * sms ? 4 : 1;
+      const int64_t per_cta = int64_t{kWarps} * t.each;
+      const unsigned grid = static_cast<unsigned>((blocks + per_cta - 1) / per_cta);
       adamw_kernel<P, G, BITS, CAP><<<grid, kWarps * 32, 0, stream>>>(t, c);
       const bcjr_status st = launched();
       if (st != BCJR_OK) return st;
@@ -366,6 +380,24 @@ bcjr_status launch_bits(const bcjr_adamw_tensor* ts, int n, int bits, Common& c,
   return bits == 8 ? launch_any<P, G, 8>(ts, n, c, stream) : launch_any<P, G, 32>(ts, n, c, stream);
 }
 
+struct Span {
+  uintptr_t begin, end;
+};
+
+// Whether no two of the parameters share memory.  Sorted in place (a heap sort: no allocation, no exception).
+bool apart(Span* spans, int n) {
+  auto less = [](const Span& a, const Span& b) { return a.begin < b.begin; };
+  bool sorted = true;
+  for (int i = 1; i < n; ++i) sorted = sorted && spans[i - 1].end <= spans[i].begin;
+  if (sorted) return true;
+  std::make_heap(spans, spans + n, less);
+  std::sort_heap(spans, spans + n, less);
+  for (int i = 1; i < n; ++i) {
+    if (spans[i - 1].end > spans[i].begin) return false;
+  }
+  return true;
+}
+
 }  // namespace
 
 extern "C" bcjr_status bcjr_adamw_step(const bcjr_adamw_tensor* tensors, int n_tensors, int param_dtype,
@@ -389,6 +421,23 @@ extern "C" bcjr_status bcjr_adamw_step(const bcjr_adamw_tensor* tensors, int n_t
     blocks += (t.numel + kBlock - 1) / kBlock;
   }
   if (blocks == 0) return BCJR_OK;
+  {
+    Span few[256];
+    std::unique_ptr<Span[]> many;
+    Span* spans = few;
+    if (n_tensors > 256) {
+      many.reset(new (std::nothrow) Span[n_tensors]);
+      if (!many) return BCJR_ERR_WORKSPACE;
+      spans = many.get();
+    }
+    int n = 0;
+    for (int i = 0; i < n_tensors; ++i) {
+      if (tensors[i].numel == 0) continue;
+      const uintptr_t at = reinterpret_cast<uintptr_t>(tensors[i].param);
+      spans[n++] = {at, at + static_cast<uintptr_t>(tensors[i].numel) * dtype_size(param_dtype)};
+    }
+    if (!apart(spans, n)) return BCJR_ERR_INVALID_ARG;
+  }
   if (!first || !second || !ptr_aligned(first, 16) || !ptr_aligned(second, 16)) return BCJR_ERR_INVALID_ARG;
   if ((state_bits == 8) != (scales != nullptr) || !ptr_aligned(scales, 4) || !ptr_aligned(o->grad_scale, 4) ||
       !ptr_aligned(o->step_ptr, 8))

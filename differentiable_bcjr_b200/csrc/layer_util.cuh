@@ -28,6 +28,20 @@ inline int sm_count() {
   return known[dev];
 }
 
+// Lets a kernel (one `most` a kernel) use up to `bytes` of dynamic shared
+// memory on the current device; asked again only for more.
+inline bool allow_shared(const void* kernel, int (&most)[64], int bytes) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  if (bytes <= most[dev]) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  most[dev] = bytes;
+  return true;
+}
+
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }

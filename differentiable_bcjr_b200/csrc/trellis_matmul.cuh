@@ -57,31 +57,80 @@ __device__ __forceinline__ uint32_t shifted(const uint32_t (&a)[N], int at) {
   return at % 32 == 0 ? a[at / 32] : __funnelshift_l(a[at / 32 + 1], a[at / 32], at % 32);
 }
 
-// The codeword of the state whose first bit is bit `at` of the chunk; false:
-// it is in the other half of the codebook.
-template <Held HELD, int N>
-__device__ __forceinline__ bool codeword(const unsigned char* table, uint32_t lane_copy, int shift, uint32_t mask,
-                                         uint32_t phase_bit, const uint32_t (&a)[N], int at, float& c) {
+__device__ __forceinline__ float shared_f32(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t shared_u16(uint32_t at) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+  return v;
+}
+
+// acc[m] += codeword * x[m] for the state whose first bit is bit `at` of the
+// chunk, where its codeword is in the half of the codebook at hand.  `table`:
+// its shared-memory address (F32: of the lane's copy).
+template <Held HELD, int MT, int N>
+__device__ __forceinline__ void add_step(uint32_t table, int shift, uint32_t mask, uint32_t phase_bit,
+                                         const uint32_t (&a)[N], int at, const float (&x)[MT], float (&acc)[MT]) {
+  float c;
   if constexpr (HELD == F32) {
     // shift and mask leave the state times the bytes between its copies
-    const uint32_t offset = ((shifted(a, at) >> shift) & mask) | lane_copy;
-    c = *reinterpret_cast<const float*>(table + offset);
-    return true;
+    c = shared_f32(table + ((shifted(a, at) >> shift) & mask));
   } else {
     // 16 bits a state: constant shifts put it above the byte offset's low bits
     constexpr int LOW = HELD == HALVES ? 2 : 1;
     const int down = 48 - at % 32 - LOW;
     const uint32_t q = down >= 32 ? a[at / 32] >> (down - 32) : __funnelshift_r(a[at / 32 + 1], a[at / 32], down);
     if constexpr (HELD == HALVES) {
-      if ((q & 0x20000u) != phase_bit) return false;
-      c = *reinterpret_cast<const float*>(table + (q & 0x1FFFCu));
+      // predicated, not multiplied by 0: an input may be infinite
+      const uint32_t from = table + (q & 0x1FFFCu), other = (q ^ phase_bit) & 0x20000u;
+      if constexpr (MT == 1) {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .f32 c;\n\t"
+            "setp.eq.u32 p, %1, 0;\n\t"
+            "@p ld.shared.f32 c, [%2];\n\t"
+            "@p fma.rn.f32 %0, c, %3, %0;\n\t}"
+            : "+f"(acc[0])
+            : "r"(other), "r"(from), "f"(x[0]));
+      } else {
+#pragma unroll
+        for (int m = 0; m < MT; m += 4) {
+          // the codeword stays in a register from the first four to the next
+          if (m == 0)
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "setp.eq.u32 p, %5, 0;\n\t"
+                "mov.f32 %4, 0f00000000;\n\t"
+                "@p ld.shared.f32 %4, [%6];\n\t"
+                "@p fma.rn.f32 %0, %4, %7, %0;\n\t"
+                "@p fma.rn.f32 %1, %4, %8, %1;\n\t"
+                "@p fma.rn.f32 %2, %4, %9, %2;\n\t"
+                "@p fma.rn.f32 %3, %4, %10, %3;\n\t}"
+                : "+f"(acc[m]), "+f"(acc[m + 1]), "+f"(acc[m + 2]), "+f"(acc[m + 3]), "=&f"(c)
+                : "r"(other), "r"(from), "f"(x[m]), "f"(x[m + 1]), "f"(x[m + 2]), "f"(x[m + 3]));
+          else
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "setp.eq.u32 p, %5, 0;\n\t"
+                "@p fma.rn.f32 %0, %4, %6, %0;\n\t"
+                "@p fma.rn.f32 %1, %4, %7, %1;\n\t"
+                "@p fma.rn.f32 %2, %4, %8, %2;\n\t"
+                "@p fma.rn.f32 %3, %4, %9, %3;\n\t}"
+                : "+f"(acc[m]), "+f"(acc[m + 1]), "+f"(acc[m + 2]), "+f"(acc[m + 3])
+                : "f"(c), "r"(other), "f"(x[m]), "f"(x[m + 1]), "f"(x[m + 2]), "f"(x[m + 3]));
+        }
+      }
+      return;
     } else if constexpr (HELD == B16) {
-      c = __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(table + (q & 0x1FFFEu))) << 16);
+      c = __uint_as_float(shared_u16(table + (q & 0x1FFFEu)) << 16);
     } else {
-      c = __half2float(*reinterpret_cast<const __half*>(table + (q & 0x1FFFEu)));
+      c = __half2float(__ushort_as_half(static_cast<uint16_t>(shared_u16(table + (q & 0x1FFFEu)))));
     }
-    return true;
   }
+#pragma unroll
+  for (int m = 0; m < MT; ++m) acc[m] = fmaf(c, x[m], acc[m]);
 }
 
 // `bytes` (a multiple of 16) into shared memory, 16 at a time where the source allows.
@@ -105,7 +154,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) trellis_matmul_kernel(const __
   const int S = 1 << p.L;
   const size_t table_bytes = HELD == F32 ? static_cast<size_t>(S) * 4 << p.copies_log2 : static_cast<size_t>(S) * 2;
   float* const sums = reinterpret_cast<float*>(smem + (table_bytes + 15) / 16 * 16) + warp * kSums;  // of [kWarps][kSums]
-  const uint32_t lane_copy = (lane & ((1u << p.copies_log2) - 1u)) * 4;
+  uint32_t table;  // kept in a register
+  asm volatile("mov.u32 %0, %1;" : "=r"(table) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(smem))));
+  if (HELD == F32) table += (lane & ((1u << p.copies_log2) - 1u)) * 4;
   const int shift = 30 - p.L - p.copies_log2;
   const uint32_t mask = (static_cast<uint32_t>(S) - 1u) << (2 + p.copies_log2);
 
@@ -202,14 +253,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) trellis_matmul_kernel(const __
               float acc[MT] = {};
 #pragma unroll
               for (int i = 0; i < CH; ++i) {
-                float c;
-                bool add = codeword<HELD>(smem, lane_copy, shift, mask, phase_bit, a, i * K, c);
-                if (!WHOLE) add = add && i < count;
-                // (a product with 0 would not do: the codeword or the input may be infinite)
-                if (add) {
-#pragma unroll
-                  for (int m = 0; m < MT; ++m) acc[m] = fmaf(c, x[i][m], acc[m]);
-                }
+                // (a step behind the end would read some state, whose codeword may be infinite)
+                if (WHOLE || i < count) add_step<HELD>(table, shift, mask, phase_bit, a, i * K, x[i], acc);
               }
 #pragma unroll
               for (int m = 0; m < MT; ++m) v[rr * MT + m] = have ? acc[m] * now_scale[rr] : 0.f;
@@ -255,13 +300,11 @@ bcjr_status launch(Params p, int sms, cudaStream_t s) {
   const size_t table = HELD == F32 ? S * 4 << p.copies_log2 : S * 2;
   const size_t smem = (table + 15) / 16 * 16 + sizeof(float) * kWarps * kSums;
   auto* const kernel = trellis_matmul_kernel<K, MT, CH, HELD>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) {
-    cudaGetLastError();
-    return BCJR_ERR_CUDA;
-  }
+  static int most[64];
+  if (!allow_shared(reinterpret_cast<const void*>(kernel), most, static_cast<int>(smem))) return BCJR_ERR_CUDA;
   const int teams = kWarps / p.wide;
-  const int most = (p.rows + teams - 1) / teams;
-  const dim3 grid(static_cast<unsigned>(most < sms ? most : sms), static_cast<unsigned>((p.tokens + MT - 1) / MT));
+  const int useful = (p.rows + teams - 1) / teams;
+  const dim3 grid(static_cast<unsigned>(useful < sms ? useful : sms), static_cast<unsigned>((p.tokens + MT - 1) / MT));
   kernel<<<grid, kWarps * 32, smem, s>>>(p);
   return launched();
 }

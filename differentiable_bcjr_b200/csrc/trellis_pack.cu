@@ -21,6 +21,7 @@ struct Params {
   int* bad;
   int L, n, words;
   int per_seq;      // pieces of a sequence
+  bool dense;       // all pieces are whole, and 16-byte aligned
   long long total;  // pieces of all sequences
 };
 
@@ -41,6 +42,19 @@ __global__ void __launch_bounds__(kWarps * 32) trellis_pack_kernel(const __grid_
   const uint32_t my_first = have ? static_cast<uint32_t>(p.states[my_seq * p.n + 32 * my_piece]) : 0u;
 
   bool bad = false;
+  if (!CHECK && p.dense && q0 + 32 <= p.total) {
+    // whole pieces that follow one another: four states a lane at a time
+    const int4* const from = reinterpret_cast<const int4*>(p.states + q0 * 32) + lane;
+    int4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __ldcs(from + i * 32);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      constexpr uint32_t low = (1u << K) - 1u;
+      const uint32_t four = (v[i].x & low) | ((v[i].y & low) << 8) | ((v[i].z & low) << 16) | ((v[i].w & low) << 24);
+      *reinterpret_cast<uint32_t*>(mine + (i * 4 + (lane >> 3)) * kPitch + (lane & 7) * 4) = four;
+    }
+  } else
 #pragma unroll 8
   for (int i = 0; i < 32; ++i) {
     uint32_t state = 0;
@@ -120,6 +134,7 @@ extern "C" bcjr_status bcjr_trellis_pack(const int32_t* states, int state_bits, 
   p.n = seq_len;
   p.words = static_cast<int>((static_cast<long long>(seq_len) * k + state_bits - k + 31) / 32);
   p.per_seq = (seq_len + 31) / 32;
+  p.dense = seq_len % 32 == 0 && ptr_aligned(states, 16);
   p.total = static_cast<long long>(p.per_seq) * n_seq;
   const long long grid = (p.total + 32 * kWarps - 1) / (32 * kWarps);
   if (grid > 0x7FFFFFFFll) return BCJR_ERR_UNSUPPORTED;

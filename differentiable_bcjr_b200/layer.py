@@ -19,35 +19,38 @@ from . import BCJRError, lib
 
 _DTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 STATE_BLOCK = 256  # elements of a block of optimiser state
 
 
 def _call(name, index, *args):
     """The library's call `name` on the current stream of device `index`."""
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         status = getattr(lib(), name)(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
             status = getattr(lib(), name)(*args, _raw_stream(index))
-    if status != 0:
+    if status:
         raise BCJRError(status, name)
 
 
 def _on_device(t, name):
-    if not t.is_cuda:
+    index = t.get_device()
+    if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor (libbcjr has no CPU path)")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t.get_device()
+    return index
 
 
 def _like(t, name, shape, dtype, index):
+    if t.get_device() == index and t.dtype is dtype and t.is_contiguous() and t.shape == shape:  # the usual case
+        return
     if _on_device(t, name) != index:
         raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
 def _dtype(t, name):
@@ -102,32 +105,27 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
         raise ValueError(f"{n} parameters and {len(grads)} gradients")
     if n == 0:
         return
-    T = torch.Tensor
     given = [g for g in grads if g is not None]
+    both = list(params) + given
     index = params[0].get_device()
-    if index < 0 or {index} != set(map(T.get_device, params)) or not {index} >= set(map(T.get_device, given)):
+    if index < 0 or set(map(_get_device, both)) != {index}:
         raise ValueError("parameters and gradients must be CUDA tensors of one device (libbcjr has no CPU path)")
-    if not (all(map(T.is_contiguous, params)) and all(map(T.is_contiguous, given))):
+    if not all(map(_is_contiguous, both)):
         raise ValueError("parameters and gradients must be contiguous")
-    kind, = _one_dtype(params, "parameters")
-    gkind = _one_dtype(given, "gradients")[0] if given else kind
+    kind = _one_dtype(params, "parameters")
+    gkind = _one_dtype(given, "gradients") if given else kind
     if kind != torch.float32 and gkind not in (torch.float32, kind):
         raise ValueError(f"{kind} parameters take gradients of {kind} or float32, not {gkind}")
-    numel = list(map(T.numel, params))
-    pp = list(map(T.data_ptr, params))
+    numel = list(map(_numel, params))
     if len(given) == n:
-        gp, gn = list(map(T.data_ptr, grads)), list(map(T.numel, grads))
-        if gn != numel:
-            raise ValueError("every gradient must have as many elements as its parameter")
+        gp, same = list(map(_data_ptr, grads)), list(map(_numel, grads)) == numel
     else:
         gp = [0 if g is None else g.data_ptr() for g in grads]
-        if any(g is not None and g.numel() != m for g, m in zip(grads, numel)):
-            raise ValueError("every gradient must have as many elements as its parameter")
-    size = 4 if kind == torch.float32 else 2
-    spans = sorted(zip(pp, numel))
-    if any(a + m * size > b for (a, m), (b, k) in zip(spans, spans[1:]) if k):
-        raise ValueError("parameters must not overlap")
-    blocks = sum([-(-m // STATE_BLOCK) for m in numel])
+        same = all(g is None or g.numel() == m for g, m in zip(grads, numel))
+    if not same:
+        raise ValueError("every gradient must have as many elements as its parameter")
+    pp = list(map(_data_ptr, params))
+    blocks = sum([m + 255 >> 8 for m in numel])
     bits = 32 if scales is None else 8
     held = torch.float32 if bits == 32 else torch.float8_e4m3fn
     flat = (blocks * STATE_BLOCK,)
@@ -136,7 +134,7 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
     if scales is not None:
         _like(scales, "scales", (2, blocks), torch.float32, index)
     o = _AdamWOptions(lr, betas[0], betas[1], eps, weight_decay, 0, None, None, seed & 0xFFFFFFFF)
-    if isinstance(step, T):
+    if isinstance(step, torch.Tensor):
         _like(step, "step", step.shape, torch.int64, index)
         if step.numel() != 1:
             raise ValueError("step must have one element")
@@ -154,16 +152,28 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
     table[0::3] = array("Q", pp)
     table[1::3] = array("Q", gp)
     table[2::3] = array("Q", numel)
-    _call("bcjr_adamw_step", index, table.buffer_info()[0], n, _DTYPE[kind], _DTYPE[gkind], bits, exp_avg.data_ptr(),
-          exp_avg_sq.data_ptr(), None if scales is None else scales.data_ptr(), ctypes.byref(o))
+    try:
+        _call("bcjr_adamw_step", index, table.buffer_info()[0], n, _DTYPE[kind], _DTYPE[gkind], bits, exp_avg.data_ptr(),
+              exp_avg_sq.data_ptr(), None if scales is None else scales.data_ptr(), ctypes.byref(o))
+    except BCJRError:
+        size = 4 if kind == torch.float32 else 2
+        spans = sorted((a, a + m * size) for a, m in zip(pp, numel) if m)
+        if any(end > start for (_, end), (start, _) in zip(spans, spans[1:])):
+            raise ValueError("parameters must not overlap") from None
+        raise
     torch.autograd.graph.increment_version(params)
 
 
+_get_device, _is_contiguous, _numel, _data_ptr = (torch.Tensor.get_device, torch.Tensor.is_contiguous, torch.Tensor.numel,
+                                                  torch.Tensor.data_ptr)
+_get_dtype = torch.Tensor.dtype.__get__
+
+
 def _one_dtype(ts, name):
-    kinds = {t.dtype for t in ts}
+    kinds = set(map(_get_dtype, ts))
     if len(kinds) != 1 or not kinds <= _DTYPE.keys():
         raise ValueError(f"{name} must all be float32, float16 or bfloat16, not {sorted(map(str, kinds))}")
-    return tuple(kinds)
+    return kinds.pop()
 
 
 def _groups(cols, group_size):
@@ -203,9 +213,11 @@ def int4_matmul(x, packed, scales, zeros=None, group_size=128, out=None):
     `int4_quantize` gives and takes them."""
     index = _on_device(x, "x")
     kind = _dtype(x, "x")
-    if x.dim() < 1 or x.shape[-1] < 1:
+    if x.dim() < 1:
         raise ValueError("x must be [..., cols]")
-    cols = x.shape[-1]
+    *lead, cols = x.shape
+    if cols < 1:
+        raise ValueError("x must have columns")
     if scales.dim() != 2:
         raise ValueError("scales must be [groups][rows]")
     rows = scales.shape[1]
@@ -213,11 +225,11 @@ def int4_matmul(x, packed, scales, zeros=None, group_size=128, out=None):
     _like(packed, "packed", (-(-rows // 16), -(-cols // 128), 1024), torch.uint8, index)
     if zeros is not None:
         _like(zeros, "zeros", scales.shape, torch.uint8, index)
-    shape = x.shape[:-1] + (rows,)
+    lead.append(rows)
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        out = x.new_empty(lead)
     else:
-        _like(out, "out", shape, x.dtype, index)
+        _like(out, "out", tuple(lead), x.dtype, index)
     _call("bcjr_int4_matmul", index, x.data_ptr(), kind, x.numel() // cols, rows, cols, packed.data_ptr(),
           scales.data_ptr(), _dtype(scales, "scales"), None if zeros is None else zeros.data_ptr(), group_size,
           out.data_ptr())
@@ -245,7 +257,7 @@ def trellis_pack(states, state_bits, k, check=False):
     if states.dim() != 2 or states.shape[1] < 1 or states.dtype != torch.int32:
         raise ValueError("states must be int32 [n_seq][seq_len]")
     n_seq, n = states.shape
-    packed = torch.empty((n_seq, trellis_words(state_bits, k, n)), dtype=torch.int32, device=states.device)
+    packed = states.new_empty((n_seq, trellis_words(state_bits, k, n)))
     bad = torch.zeros(1, dtype=torch.int32, device=states.device) if check else None
     _call("bcjr_trellis_pack", index, states.data_ptr(), state_bits, k, n, n_seq, packed.data_ptr(),
           None if bad is None else bad.data_ptr())
@@ -264,9 +276,11 @@ def trellis_matmul(x, packed, codebook, state_bits, k, seq_len, scales=None, gro
     seq_len.  Products and sums are float32."""
     index = _on_device(x, "x")
     kind = _dtype(x, "x")
-    if x.dim() < 1 or x.shape[-1] < 1:
+    if x.dim() < 1:
         raise ValueError("x must be [..., cols]")
-    cols = x.shape[-1]
+    *lead, cols = x.shape
+    if cols < 1:
+        raise ValueError("x must have columns")
     if seq_len < 1 or cols % seq_len:
         raise ValueError("a row must be whole sequences")
     seqs = cols // seq_len
@@ -281,11 +295,11 @@ def trellis_matmul(x, packed, codebook, state_bits, k, seq_len, scales=None, gro
                                (group_size % 16 == 0 and group_size > 0 and seq_len % group_size == 0)):
             raise ValueError("group_size must be 0, a multiple of seq_len that divides cols, or a multiple of 16 that divides seq_len")
         _like(scales, "scales", (cols // group_size if group_size else 1, rows), torch.float32, index)
-    shape = x.shape[:-1] + (rows,)
+    lead.append(rows)
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        out = x.new_empty(lead)
     else:
-        _like(out, "out", shape, x.dtype, index)
+        _like(out, "out", tuple(lead), x.dtype, index)
     _call("bcjr_trellis_matmul", index, x.data_ptr(), kind, x.numel() // cols, rows, cols, packed.data_ptr(),
           codebook.data_ptr(), _dtype(codebook, "codebook"), state_bits, k, seq_len,
           None if scales is None else scales.data_ptr(), group_size, out.data_ptr())
