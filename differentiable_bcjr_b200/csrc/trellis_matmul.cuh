@@ -33,6 +33,8 @@ using Params = TrellisMatmulParams;
 constexpr int kWarps = 16;
 constexpr int kSums = 512;  // row sums a warp can hold in shared memory
 
+constexpr uint32_t kHalf = 131072;  // bytes of 2^15 float32 codewords, or 2^16 of 16 bits
+
 enum Held { F32, B16, H16, HALVES };
 
 // The sums over the warp of eight values a lane: lane l gets in v[0] that of value l >> 2.
@@ -68,91 +70,104 @@ __device__ __forceinline__ uint32_t shared_u16(uint32_t at) {
   return v;
 }
 
-// acc[m] += codeword * x[m] for the state whose first bit is bit `at` of the
-// chunk, where its codeword is in the half of the codebook at hand.  `table`:
-// its shared-memory address (F32: of the lane's copy).
-template <Held HELD, int MT, int N>
-__device__ __forceinline__ void add_step(uint32_t table, int shift, uint32_t mask, uint32_t phase_bit,
-                                         const uint32_t (&a)[N], int at, const float (&x)[MT], float (&acc)[MT]) {
-  float c;
+// The codeword of the state whose first bit is bit `at` of the chunk; 0 where
+// it is in the other half of the codebook.  `table`: its shared-memory address
+// (F32: of the lane's copy; HALVES: a zero follows the half).
+template <Held HELD, int N>
+__device__ __forceinline__ float codeword(uint32_t table, int shift, uint32_t mask, uint32_t phase_bit,
+                                          const uint32_t (&a)[N], int at, bool& here) {
+  here = true;
   if constexpr (HELD == F32) {
     // shift and mask leave the state times the bytes between its copies
-    c = shared_f32(table + ((shifted(a, at) >> shift) & mask));
+    return shared_f32(table + ((shifted(a, at) >> shift) & mask));
   } else {
     // 16 bits a state: constant shifts put it above the byte offset's low bits
     constexpr int LOW = HELD == HALVES ? 2 : 1;
     const int down = 48 - at % 32 - LOW;
     const uint32_t q = down >= 32 ? a[at / 32] >> (down - 32) : __funnelshift_r(a[at / 32 + 1], a[at / 32], down);
     if constexpr (HELD == HALVES) {
-      // predicated, not multiplied by 0: an input may be infinite
-      const uint32_t from = table + (q & 0x1FFFCu), other = (q ^ phase_bit) & 0x20000u;
-      if constexpr (MT == 1) {
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t.reg .f32 c;\n\t"
-            "setp.eq.u32 p, %1, 0;\n\t"
-            "@p ld.shared.f32 c, [%2];\n\t"
-            "@p fma.rn.f32 %0, c, %3, %0;\n\t}"
-            : "+f"(acc[0])
-            : "r"(other), "r"(from), "f"(x[0]));
-      } else {
-#pragma unroll
-        for (int m = 0; m < MT; m += 4) {
-          // the codeword stays in a register from the first four to the next
-          if (m == 0)
-            asm volatile(
-                "{\n\t.reg .pred p;\n\t"
-                "setp.eq.u32 p, %5, 0;\n\t"
-                "mov.f32 %4, 0f00000000;\n\t"
-                "@p ld.shared.f32 %4, [%6];\n\t"
-                "@p fma.rn.f32 %0, %4, %7, %0;\n\t"
-                "@p fma.rn.f32 %1, %4, %8, %1;\n\t"
-                "@p fma.rn.f32 %2, %4, %9, %2;\n\t"
-                "@p fma.rn.f32 %3, %4, %10, %3;\n\t}"
-                : "+f"(acc[m]), "+f"(acc[m + 1]), "+f"(acc[m + 2]), "+f"(acc[m + 3]), "=&f"(c)
-                : "r"(other), "r"(from), "f"(x[m]), "f"(x[m + 1]), "f"(x[m + 2]), "f"(x[m + 3]));
-          else
-            asm volatile(
-                "{\n\t.reg .pred p;\n\t"
-                "setp.eq.u32 p, %5, 0;\n\t"
-                "@p fma.rn.f32 %0, %4, %6, %0;\n\t"
-                "@p fma.rn.f32 %1, %4, %7, %1;\n\t"
-                "@p fma.rn.f32 %2, %4, %8, %2;\n\t"
-                "@p fma.rn.f32 %3, %4, %9, %3;\n\t}"
-                : "+f"(acc[m]), "+f"(acc[m + 1]), "+f"(acc[m + 2]), "+f"(acc[m + 3])
-                : "f"(c), "r"(other), "f"(x[m]), "f"(x[m + 1]), "f"(x[m + 2]), "f"(x[m + 3]));
-        }
-      }
-      return;
+      const uint32_t offset = (q ^ phase_bit) & 0x3FFFCu;  // 2^17 and more: in the other half
+      here = offset < kHalf;
+      return shared_f32(table + min(offset, kHalf));
     } else if constexpr (HELD == B16) {
-      c = __uint_as_float(shared_u16(table + (q & 0x1FFFEu)) << 16);
+      return __uint_as_float(shared_u16(table + (q & 0x1FFFEu)) << 16);
     } else {
-      c = __half2float(__ushort_as_half(static_cast<uint16_t>(shared_u16(table + (q & 0x1FFFEu)))));
+      return __half2float(__ushort_as_half(static_cast<uint16_t>(shared_u16(table + (q & 0x1FFFEu)))));
     }
   }
-#pragma unroll
-  for (int m = 0; m < MT; ++m) acc[m] = fmaf(c, x[m], acc[m]);
 }
 
-// `bytes` (a multiple of 16) into shared memory, 16 at a time where the source allows.
-__device__ __forceinline__ void copy_in(unsigned char* to, const unsigned char* from, int bytes) {
+__device__ __forceinline__ bool finite_bits(uint32_t bits, uint32_t exponent) { return (bits & exponent) != exponent; }
+
+// 2^17 bytes of codewords into shared memory, 16 at a time where the source
+// allows.  False if this thread met one that is not finite; `exponent`: the
+// exponent field of one, or of the upper of two in a word.
+template <int BYTES>
+__device__ __forceinline__ bool copy_in(unsigned char* to, const unsigned char* from, uint32_t exponent) {
+  bool fine = true;
+  auto check = [&](uint32_t w) {
+    fine = fine && finite_bits(w, exponent);
+    if (BYTES == 2) fine = fine && finite_bits(w << 16, exponent);
+  };
   if ((reinterpret_cast<uintptr_t>(from) & 15) == 0) {
 #pragma unroll 8
-    for (int i = threadIdx.x; i < bytes / 16; i += kWarps * 32) reinterpret_cast<uint4*>(to)[i] = reinterpret_cast<const uint4*>(from)[i];
+    for (int i = threadIdx.x; i < static_cast<int>(kHalf / 16); i += kWarps * 32) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(from) + i);
+      reinterpret_cast<uint4*>(to)[i] = v;
+      check(v.x);
+      check(v.y);
+      check(v.z);
+      check(v.w);
+    }
   } else {
-    for (int i = threadIdx.x; i < bytes / 2; i += kWarps * 32) reinterpret_cast<uint16_t*>(to)[i] = reinterpret_cast<const uint16_t*>(from)[i];
+    for (int i = threadIdx.x; i < static_cast<int>(kHalf / BYTES); i += kWarps * 32) {
+      if (BYTES == 2) {
+        const uint16_t v = reinterpret_cast<const uint16_t*>(from)[i];
+        reinterpret_cast<uint16_t*>(to)[i] = v;
+        check(static_cast<uint32_t>(v) << 16);
+      } else {
+        const uint32_t v = reinterpret_cast<const uint32_t*>(from)[i];
+        reinterpret_cast<uint32_t*>(to)[i] = v;
+        check(v);
+      }
+    }
   }
+  return fine;
 }
+
+// Sums of MT tokens, two to a packed multiply-add where there are several.
+template <int MT>
+struct Sums {
+  float2 v[MT / 2];
+  __device__ __forceinline__ void add(float c, const Sums& x) {
+#pragma unroll
+    for (int m = 0; m < MT / 2; ++m) v[m] = __ffma2_rn(make_float2(c, c), x.v[m], v[m]);
+  }
+  __device__ __forceinline__ float get(int m) const { return m & 1 ? v[m / 2].y : v[m / 2].x; }
+  __device__ __forceinline__ void set(int m, float f) {
+    if (m & 1) v[m / 2].y = f;
+    else v[m / 2].x = f;
+  }
+};
+template <>
+struct Sums<1> {
+  float v;
+  __device__ __forceinline__ void add(float c, const Sums& x) { v = fmaf(c, x.v, v); }
+  __device__ __forceinline__ float get(int) const { return v; }
+  __device__ __forceinline__ void set(int, float f) { v = f; }
+};
 
 template <int K, int MT, int CH, Held HELD>
 __global__ void __launch_bounds__(kWarps * 32, 1) trellis_matmul_kernel(const __grid_constant__ Params p) {
-  constexpr int ROWS = 8 / MT;  // rows whose sums are added over the warp together
+  constexpr int ROWS = 8 / MT;               // rows whose sums are added over the warp together
+  constexpr int BATCH = ROWS < 4 ? 4 : ROWS; // rows whose words are fetched together
   // a chunk starts at a multiple of CH K bits, so at worst at this bit of a word
   constexpr int STEP = (CH * K) % 32 == 0 ? 32 : (CH * K) % 16 == 0 ? 16 : 8;
   constexpr int WORDS = (32 - STEP + (CH - 1) * K + 16 + 31) / 32;
   extern __shared__ __align__(16) unsigned char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int S = 1 << p.L;
-  const size_t table_bytes = HELD == F32 ? static_cast<size_t>(S) * 4 << p.copies_log2 : static_cast<size_t>(S) * 2;
+  const size_t table_bytes = HELD == F32 ? static_cast<size_t>(S) * 4 << p.copies_log2 : HELD == HALVES ? kHalf + 16 : kHalf;
   float* const sums = reinterpret_cast<float*>(smem + (table_bytes + 15) / 16 * 16) + warp * kSums;  // of [kWarps][kSums]
   uint32_t table;  // kept in a register
   asm volatile("mov.u32 %0, %1;" : "=r"(table) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(smem))));
@@ -170,6 +185,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) trellis_matmul_kernel(const __
   const int tokens = min(MT, p.tokens - token0);
 
   constexpr int PHASES = HELD == HALVES ? 2 : 1;
+  bool all_finite = true;  // every codeword at hand is
   for (int r0 = r_begin; r0 < r_end; r0 += ROOM * teams) {
     const int r1 = min(r0 + ROOM * teams, r_end);
     for (int i = lane; i < kSums; i += 32) sums[i] = 0.f;
@@ -177,14 +193,20 @@ __global__ void __launch_bounds__(kWarps * 32, 1) trellis_matmul_kernel(const __
     for (int phase = 0; phase < PHASES; ++phase) {
       if (HELD == HALVES || r0 == r_begin) {
         if (HELD == HALVES) __syncthreads();  // the last half's readers are done
+        bool fine = true;
         if constexpr (HELD == F32) {
 #pragma unroll 8
-          for (int i = threadIdx.x; i < (S << p.copies_log2); i += kWarps * 32)
-            reinterpret_cast<float*>(smem)[i] = load_as_f32(p.codebook, p.c_dtype, i >> p.copies_log2);
+          for (int i = threadIdx.x; i < (S << p.copies_log2); i += kWarps * 32) {
+            const float v = load_as_f32(p.codebook, p.c_dtype, i >> p.copies_log2);
+            reinterpret_cast<float*>(smem)[i] = v;
+            fine = fine && finite_bits(__float_as_uint(v), 0x7F800000u);
+          }
         } else {
-          copy_in(smem, static_cast<const unsigned char*>(p.codebook) + phase * 131072, 131072);
+          const unsigned char* const from = static_cast<const unsigned char*>(p.codebook) + phase * kHalf;
+          if (HELD == HALVES && threadIdx.x == 0) *reinterpret_cast<float*>(smem + kHalf) = 0.f;
+          fine = copy_in<HELD == HALVES ? 4 : 2>(smem, from, HELD == H16 ? 0x7C000000u : 0x7F800000u);
         }
-        __syncthreads();
+        all_finite = __syncthreads_and(fine) != 0;
       }
       const uint32_t phase_bit = phase ? 0x20000u : 0u;
       for (int tile = place; tile < tiles; tile += p.wide) {
@@ -192,14 +214,19 @@ __global__ void __launch_bounds__(kWarps * 32, 1) trellis_matmul_kernel(const __
         const bool have = q < p.chunks;
         const int seq = (have ? q : 0) / p.per_seq;
         const int t0 = ((have ? q : 0) - seq * p.per_seq) * CH;
-        const int count = min(CH, p.n - t0);
+        const int count = have ? min(CH, p.n - t0) : 0;
         const int col = seq * p.n + t0;
-        float x[CH][MT];
+        Sums<MT> x[CH];
+        bool fine = all_finite;
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           const size_t at = static_cast<size_t>(token0 + min(m, tokens - 1)) * p.cols + col;
 #pragma unroll
-          for (int i = 0; i < CH; ++i) x[i][m] = i < count ? load_as_f32(p.x, p.x_dtype, at + i) : 0.f;
+          for (int i = 0; i < CH; ++i) {
+            const float v = i < count ? load_as_f32(p.x, p.x_dtype, at + i) : 0.f;
+            x[i].set(m, v);
+            fine = fine && finite_bits(__float_as_uint(v), 0x7F800000u);
+          }
         }
         const int bit = t0 * K, skew = bit & 31;
         const uint32_t* const stream = p.packed + static_cast<size_t>(seq) * p.words;
@@ -209,13 +236,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1) trellis_matmul_kernel(const __
         const size_t row_words = static_cast<size_t>(p.seqs) * p.words;
         const float* const scale = p.scales ? p.scales + static_cast<size_t>(col / p.group) * p.rows : nullptr;
 
-        auto walk = [&](auto whole) {
-          constexpr bool WHOLE = decltype(whole)::value;  // every lane's chunk has all CH steps
-          uint32_t next[ROWS][WORDS];
-          float next_scale[ROWS];
+        // GUARDED: a step behind the chunk's end and a state of the other half
+        // are left out.  Otherwise they are a product with 0, which is enough
+        // where codewords and inputs are finite.
+        auto walk = [&](auto guarded) {
+          constexpr bool GUARDED = decltype(guarded)::value;
+          uint32_t next[BATCH][WORDS];
+          float next_scale[BATCH];
           auto fetch = [&](int rb) {
 #pragma unroll
-            for (int rr = 0; rr < ROWS; ++rr) {
+            for (int rr = 0; rr < BATCH; ++rr) {
               if (rb + rr >= r1) break;
               const uint32_t* const from = stream + (rb + rr) * row_words;
 #pragma unroll
@@ -223,60 +253,66 @@ __global__ void __launch_bounds__(kWarps * 32, 1) trellis_matmul_kernel(const __
               next_scale[rr] = scale ? __ldg(scale + rb + rr) : 1.f;
             }
           };
-          fetch(r0 + team * ROWS);
-          for (int rb = r0 + team * ROWS; rb < r1; rb += teams * ROWS) {
-            uint32_t now[ROWS][WORDS];
-            float now_scale[ROWS];
+          fetch(r0 + team * BATCH);
+          int at_sum = 0;  // of the team's sums
+          for (int rb = r0 + team * BATCH; rb < r1; rb += teams * BATCH) {
+            uint32_t now[BATCH][WORDS];
+            float now_scale[BATCH];
 #pragma unroll
-            for (int rr = 0; rr < ROWS; ++rr) {
+            for (int rr = 0; rr < BATCH; ++rr) {
 #pragma unroll
               for (int i = 0; i < WORDS; ++i) now[rr][i] = next[rr][i];
               now_scale[rr] = next_scale[rr];
             }
-            fetch(rb + teams * ROWS);
-            float v[8];
+            fetch(rb + teams * BATCH);
 #pragma unroll
-            for (int rr = 0; rr < ROWS; ++rr) {
-              if (rb + rr >= r1) {
+            for (int r8 = 0; r8 < BATCH; r8 += ROWS) {
+              if (rb + r8 >= r1) break;
+              float v[8];
 #pragma unroll
-                for (int m = 0; m < MT; ++m) v[rr * MT + m] = 0.f;
-                continue;
+              for (int rr = 0; rr < ROWS; ++rr) {
+                Sums<MT> acc;
+#pragma unroll
+                for (int m = 0; m < MT; ++m) acc.set(m, 0.f);
+                if (rb + r8 + rr < r1) {
+                  uint32_t a[WORDS + 1];
+#pragma unroll
+                  for (int i = 0; i < WORDS; ++i) a[i] = now[r8 + rr][i];
+                  a[WORDS] = 0;
+                  if constexpr (STEP != 32) {
+#pragma unroll
+                    for (int i = 0; i < WORDS; ++i) a[i] = __funnelshift_l(a[i + 1], a[i], skew);
+                  }
+#pragma unroll
+                  for (int i = 0; i < CH; ++i) {
+                    bool here;
+                    const float c = codeword<HELD>(table, shift, mask, phase_bit, a, i * K, here);
+                    if (!GUARDED || (here && i < count)) acc.add(c, x[i]);
+                  }
+                }
+#pragma unroll
+                for (int m = 0; m < MT; ++m) v[rr * MT + m] = acc.get(m) * now_scale[r8 + rr];
               }
-              uint32_t a[WORDS + 1];
-#pragma unroll
-              for (int i = 0; i < WORDS; ++i) a[i] = now[rr][i];
-              a[WORDS] = 0;
-              if constexpr (STEP != 32) {
-#pragma unroll
-                for (int i = 0; i < WORDS; ++i) a[i] = __funnelshift_l(a[i + 1], a[i], skew);
+              sum8(v, lane);
+              if ((lane & 3) == 0) {
+                const int i = lane >> 2;
+                if (rb + r8 + i / MT < r1) sums[at_sum + r8 * MT + i] += v[0];
               }
-              float acc[MT] = {};
-#pragma unroll
-              for (int i = 0; i < CH; ++i) {
-                // (a step behind the end would read some state, whose codeword may be infinite)
-                if (WHOLE || i < count) add_step<HELD>(table, shift, mask, phase_bit, a, i * K, x[i], acc);
-              }
-#pragma unroll
-              for (int m = 0; m < MT; ++m) v[rr * MT + m] = have ? acc[m] * now_scale[rr] : 0.f;
             }
-            sum8(v, lane);
-            if ((lane & 3) == 0) {
-              const int i = lane >> 2, rr = i / MT, m = i % MT;
-              if (rb + rr < r1) sums[((rb - r0) / (teams * ROWS) * ROWS + rr) * MT + m] += v[0];
-            }
+            at_sum += BATCH * MT;
             __syncwarp();
           }
         };
-        if (__all_sync(~0u, count == CH)) walk(std::true_type{});
-        else walk(std::false_type{});
+        if (__all_sync(~0u, fine)) walk(std::false_type{});
+        else walk(std::true_type{});
       }
     }
     __syncthreads();
     const float* const all = sums - warp * kSums;
     for (int i = threadIdx.x; i < (r1 - r0) * tokens; i += kWarps * 32) {
       const int row = i % (r1 - r0), m = i / (r1 - r0);
-      const int turn = row / (teams * ROWS), of = row % (teams * ROWS);
-      const float* const from = all + (of / ROWS * p.wide) * kSums + (turn * ROWS + of % ROWS) * MT + m;
+      const int turn = row / (teams * BATCH), of = row % (teams * BATCH);
+      const float* const from = all + (of / BATCH * p.wide) * kSums + (turn * BATCH + of % BATCH) * MT + m;
       float v = 0.f;
       for (int w = 0; w < p.wide; ++w) v += from[w * kSums];
       store_from_f32(p.y, p.x_dtype, static_cast<size_t>(token0 + m) * p.rows + r0 + row, v);
@@ -297,7 +333,7 @@ bcjr_status launch(Params p, int sms, cudaStream_t s) {
   if (HELD == F32) {
     while (p.copies_log2 < 5 && (S * 4 << (p.copies_log2 + 1)) <= (128u << 10)) ++p.copies_log2;
   }
-  const size_t table = HELD == F32 ? S * 4 << p.copies_log2 : S * 2;
+  const size_t table = HELD == F32 ? S * 4 << p.copies_log2 : HELD == HALVES ? kHalf + 16 : kHalf;
   const size_t smem = (table + 15) / 16 * 16 + sizeof(float) * kWarps * kSums;
   auto* const kernel = trellis_matmul_kernel<K, MT, CH, HELD>;
   static int most[64];
@@ -312,7 +348,7 @@ bcjr_status launch(Params p, int sms, cudaStream_t s) {
 template <int K, Held HELD>
 bcjr_status launch_tokens(const Params& p, int sms, cudaStream_t s) {
   if (p.tokens == 1) return launch<K, 1, 16, HELD>(p, sms, s);
-  if (p.tokens <= 4) return launch<K, 4, 16, HELD>(p, sms, s);
+  if (p.tokens <= 4) return launch<K, 4, 8, HELD>(p, sms, s);
   return launch<K, 8, 8, HELD>(p, sms, s);
 }
 

@@ -12,13 +12,17 @@ mean((X W^T - X W_hat(V)^T)^2) with W_hat the BCJR soft codeword of V (the
 library's forward and backward calls through autograd).  At the end V is
 hard-decoded with the Viterbi call and compared with decoding W directly.
 The matrix products are ordinary PyTorch; every trellis step runs in the
-library's kernels.
+library's kernels, and on request the optimiser step (`optimizer="adamw"` or
+"adamw8"), the packed layer that the result is served as (`pack`) and the
+4-bit rounding it is compared with (`int4_group_size`).
 """
 from __future__ import annotations
 
 import torch
 
 from . import soft_quantize, viterbi_decode
+from .linear import Int4Linear, TrellisLinear
+from .optim import AdamW
 
 
 def _recon_mse(X, W_ref, W_q):
@@ -27,16 +31,31 @@ def _recon_mse(X, W_ref, W_q):
 
 def layer_reconstruction_qat(W: torch.Tensor, X: torch.Tensor, codebook: torch.Tensor, state_bits: int, k: int,
                              seq_len: int, temperatures, steps_per_temperature: int = 10, lr: float = 0.02,
-                             train_codebook: bool = False):
+                             train_codebook: bool = False, optimizer: str = "adam", pack: bool = False,
+                             int4_group_size: int | None = None):
     """Returns a dict with the loss history, the hard-decoded reconstruction MSE
     after QAT (`mse_qat`), that of decoding W directly (`mse_ptq`), and the
-    quantised weights."""
+    quantised weights.
+
+    optimizer: "adam" is torch.optim.Adam; "adamw" and "adamw8" are the
+    library's fused step (without weight decay, the same update) with moments
+    in 32 and 8 bits.  pack: the result also holds `linear`, the trained layer
+    packed at k bits a weight (rows must be whole sequences).  int4_group_size:
+    it also holds `mse_int4`, the error of rounding W to 4 bits in groups of
+    that many columns."""
     if W.numel() % seq_len:
         raise ValueError("the layer must split into whole sequences")
+    if optimizer not in ("adam", "adamw", "adamw8"):
+        raise ValueError("optimizer must be adam, adamw or adamw8")
+    if pack and W.shape[1] % seq_len:
+        raise ValueError("to be packed, the layer's rows must be whole sequences")
     V = W.detach().clone().requires_grad_(True)
     cb = codebook.detach().clone().requires_grad_(train_codebook)
     params = [V] + ([cb] if train_codebook else [])
-    opt = torch.optim.Adam(params, lr=lr)
+    if optimizer == "adam":
+        opt = torch.optim.Adam(params, lr=lr)
+    else:
+        opt = AdamW(params, lr=lr, state_bits=8 if optimizer == "adamw8" else 32)
     history = []
     for T in temperatures:
         for _ in range(steps_per_temperature):
@@ -53,5 +72,11 @@ def layer_reconstruction_qat(W: torch.Tensor, X: torch.Tensor, codebook: torch.T
         w_ptq = w_ptq.view_as(W)
         mse_qat = float(_recon_mse(X, W, w_qat))
         mse_ptq = float(_recon_mse(X, W, w_ptq))
-    return {"history": [float(h) for h in history], "mse_qat": mse_qat, "mse_ptq": mse_ptq,
-            "w_qat": w_qat, "w_ptq": w_ptq, "preimage": V.detach(), "codebook": cb.detach()}
+        result = {"history": [float(h) for h in history], "mse_qat": mse_qat, "mse_ptq": mse_ptq,
+                  "w_qat": w_qat, "w_ptq": w_ptq, "preimage": V.detach(), "codebook": cb.detach()}
+        if pack:
+            result["linear"] = TrellisLinear.from_weight(V, cb.detach(), state_bits, k, seq_len)
+        if int4_group_size is not None:
+            int4 = Int4Linear.from_weight(W, int4_group_size)
+            result["mse_int4"] = float(((X @ W.T - int4(X.contiguous())) ** 2).mean())
+    return result
