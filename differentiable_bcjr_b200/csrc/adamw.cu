@@ -72,12 +72,22 @@ __device__ __forceinline__ uint32_t hash_bits(uint32_t h) {
   return h ^ (h >> 15);
 }
 
-// Magnitude code of x, scaled so that its block's largest is 448 2^-120: a
-// float's exponent field is then e4m3's, so the code is the float's bits cut
+// The code of a magnitude x, scaled so that its block's largest is 448 2^-120:
+// a float's exponent field is then e4m3's, so the code is the float's bits cut
 // after three mantissa bits; the 20 bits that fall away decide the rounding
-// together with `rnd`, which is below 2^20 - 4, so that the largest (at most
-// a few places off 448) does not round up.
-__device__ __forceinline__ uint32_t e4m3_code(float x, uint32_t rnd) { return (__float_as_uint(x) + rnd) >> 20; }
+// together with `random`, 16 bits and a half.  Sixteen times their sum has the
+// code in its upper byte.  The largest (at most a few places off 448) does not
+// round up, since random is at least eight places short of a whole step.
+__device__ __forceinline__ uint32_t e4m3_upper(float x, uint32_t random) {
+  uint32_t d;  // (a multiply-add, where a shift and an add would load the busier integer pipe)
+  asm("mad.lo.u32 %0, %1, 16, %2;" : "=r"(d) : "r"(__float_as_uint(x)), "r"(random));
+  return d;
+}
+
+// The upper bytes of four words.
+__device__ __forceinline__ uint32_t upper_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
+}
 
 // Byte i of a word as a float times 2^-120, exactly (subnormal codes are subnormal floats).
 template <bool SIGNED>
@@ -89,11 +99,6 @@ __device__ __forceinline__ float e4m3_small(uint32_t w, int i) {
 __device__ __forceinline__ float sqrt_approx(float v) {  // within 2^-23 of the root, denormals included
   float r;
   asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-__device__ __forceinline__ float sqrt_approx_ftz(float v) {  // the same, 0 below 2^-126
-  float r;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
 __device__ __forceinline__ float rcp_approx(float v) {  // within 2^-23; 0 above 2^126
@@ -165,14 +170,22 @@ __device__ __forceinline__ void store8(T* base, int lane, int limit, const T (&v
   }
 }
 
-// m, v and p of one element; r = sqrt(v).  Each product and sum of m and v is
-// rounded on its own, so that a rounding decision of the 8-bit codes does not
-// depend on how the compiler contracts them.
+// m, v and p of one element; r = sqrt(v).  8-bit codes are rounded from m and
+// r: there every operation on the way is rounded by itself and correctly, so
+// that a code does not hang on how the compiler contracts products and sums
+// (one code more or less is a sixteenth of the value, far over what the
+// parameter's float32 arithmetic leaves).
 template <int BITS>
 __device__ __forceinline__ float advance(float& m, float& v, float& r, float g, float p, const Scalars& s) {
-  m = __fadd_rn(__fmul_rn(m, s.b1), __fmul_rn(g, s.c1));
-  v = __fadd_rn(__fmul_rn(v, s.b2), __fmul_rn(__fmul_rn(g, g), s.c2));
-  r = BITS == 32 ? sqrt_approx(v) : sqrt_approx_ftz(v);
+  if constexpr (BITS == 32) {
+    m = fmaf(m, s.b1, g * s.c1);
+    v = fmaf(v, s.b2, g * g * s.c2);
+    r = sqrt_approx(v);
+  } else {
+    m = __fadd_rn(__fmul_rn(m, s.b1), __fmul_rn(g, s.c1));
+    v = __fadd_rn(__fmul_rn(v, s.b2), __fmul_rn(__fmul_rn(g, g), s.c2));
+    r = __fsqrt_rn(v);
+  }
   const float step = m * rcp_approx(fmaf(r, s.inv_sqrt_bc2, s.eps));
   return fmaf(-s.lr_bc1, step, p * s.decay);
 }
@@ -248,8 +261,8 @@ __device__ __forceinline__ void block_step8(P* p, const G* g, const Common& c, c
   const float top_a = __uint_as_float(__reduce_max_sync(~0u, ta) >> 1);
   const float top_b = __uint_as_float(__reduce_max_sync(~0u, tb) & 0x7FFFFFFFu);
   const bool held_a = !(top_a < kTiny), held_b = !(top_b < kTiny);
-  float inv_a = held_a ? __fmul_rn(rcp_approx(top_a), 448.f) : 0.f, inv_b = held_b ? __fmul_rn(rcp_approx(top_b), 448.f) : 0.f;
-  const uint32_t least_b = held_b ? 1u : 0u;  // r > 0 does not become 0
+  float inv_a = held_a ? __fmul_rn(__frcp_rn(top_a), 448.f) : 0.f, inv_b = held_b ? __fmul_rn(__frcp_rn(top_b), 448.f) : 0.f;
+  const uint32_t least_b = held_b ? 1u << 24 : 0u;  // r > 0 (then it is over 2^-75) does not become 0
   // The factor 2^-120 goes into the reciprocal where that stays a normal float.
   float small = 1.f;
   if (inv_a >= 0x1p-5f && inv_b >= 0x1p-5f) {
@@ -259,6 +272,7 @@ __device__ __forceinline__ void block_step8(P* p, const G* g, const Common& c, c
     small = 0x1p-120f;
   }
   uint32_t h0 = (static_cast<uint32_t>(block * kBlock) + element_of<MAP>(lane, 0)) * kHashA + s.mix;
+  uint32_t ua[8], ub[8];
   auto encode = [&](auto scaled_twice) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -268,14 +282,21 @@ __device__ __forceinline__ void block_step8(P* p, const G* g, const Common& c, c
         x = __fmul_rn(x, small);
         y = __fmul_rn(y, small);
       }
-      const uint32_t ca = e4m3_code(x, ((h >> 12) & 0xFFFF0u) | 8u);
-      const uint32_t cb = e4m3_code(y, ((h << 4) & 0xFFFF0u) | 8u);
-      a[i] = static_cast<uint8_t>(ca | ((__float_as_uint(m[i]) >> 24) & 0x80u));
-      b[i] = static_cast<uint8_t>(max(cb, min(__float_as_uint(r[i]), least_b)));
+      ua[i] = e4m3_upper(x, ((h >> 8) & 0xFFFF00u) | 0x80u);
+      ub[i] = e4m3_upper(y, ((h << 8) & 0xFFFF00u) | 0x80u);
+      ua[i] = (ua[i] & 0x7FFFFFFFu) | (__float_as_uint(m[i]) & 0x80000000u);
+      ub[i] = max(ub[i], min(__float_as_uint(r[i]), least_b));
     }
   };
   if (small == 1.f) encode(std::false_type{});
   else encode(std::true_type{});
+#pragma unroll
+  for (int i = 0; i < 8; i += 4) {
+    wa[i >> 2] = upper_bytes(ua[i], ua[i + 1], ua[i + 2], ua[i + 3]);
+    wb[i >> 2] = upper_bytes(ub[i], ub[i + 1], ub[i + 2], ub[i + 3]);
+  }
+  memcpy(a, wa, 8);
+  memcpy(b, wb, 8);
   if (lane == 0) {
     c.scales[block] = held_a ? __fmul_rn(top_a, 1.f / 448.f) : 0.f;
     c.scales[c.all_blocks + block] = held_b ? __fmul_rn(top_b, 1.f / 448.f) : 0.f;
