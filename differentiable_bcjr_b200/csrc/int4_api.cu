@@ -10,9 +10,9 @@ extern "C" bcjr_status bcjr_int4_matmul(const void* x, int x_dtype, int tokens, 
   if (!dtype_ok(x_dtype) || !dtype_ok(scale_dtype) || tokens < 0 || rows < 0 || cols < 1 || group_size < 0)
     return BCJR_ERR_INVALID_ARG;
   if (group_size % 128 != 0 && group_size != 32 && group_size != 64) return BCJR_ERR_UNSUPPORTED;
-  // passes are the third grid dimension, row tiles times the split the first;
+  // passes (of at least 10 tokens) are the third grid dimension, row tiles times the split the first;
   // a block's group comes out of a float product, exact below 2^21 blocks
-  if (tokens > 65535 || rows > (1 << 30) || cols > (1 << 27)) return BCJR_ERR_UNSUPPORTED;
+  if (tokens > 10 * 65535 || rows > (1 << 30) || cols > (1 << 27)) return BCJR_ERR_UNSUPPORTED;
   if (tokens == 0 || rows == 0) return BCJR_OK;
   if (!x || !packed || !scales || !y || !ptr_aligned(packed, 16) || !ptr_aligned(x, dtype_size(x_dtype)) ||
       !ptr_aligned(y, dtype_size(x_dtype)) || !ptr_aligned(scales, dtype_size(scale_dtype)))

@@ -5,8 +5,7 @@
 // word of the packed tile, so a lane reads 16 or 32 contiguous bytes and
 // writes one word, four blocks' loads ahead of the work on them.  Groups of 32,
 // 64 and 128 columns are 4, 8 and 16
-// neighbouring lanes, their extremes a few shuffles.  Longer groups take two
-// passes over their blocks, the second from the cache.  Reading w bounds the
+// neighbouring lanes, their extremes a few shuffles.  Reading w bounds the
 // call (4.5 B a weight for float32 moved in all, 2.5 B for 16-bit types).
 #include <cmath>
 #include <cstring>
@@ -25,6 +24,7 @@ struct Params {
   int group_blocks;         // of a group; 0: groups shorter than a block
   int lanes;                // lanes of a group within its block (4, 8 or 16)
   int groups;
+  unsigned units;           // CTAs of a tile's columns
   uint8_t* packed;
   void* scales;
   int scale_dtype;
@@ -134,54 +134,78 @@ template <typename T, bool ZERO>
 __global__ void __launch_bounds__(kWarps * 32) int4_quantize_kernel(const __grid_constant__ Params p) {
   const int lane = threadIdx.x & 31, l16 = lane & 15;
   const int row16 = (threadIdx.x >> 5) * 2 + (lane >> 4);
-  const int tile = blockIdx.y;
+  const int tile = static_cast<int>(blockIdx.x / p.units);
   const int row = tile * 16 + row16;
   const bool ok = row < p.rows;
   const T* const src = static_cast<const T*>(p.w) + static_cast<size_t>(ok ? row : p.rows - 1) * p.cols;
   const bool fast = (p.cols * sizeof(T)) % 16 == 0 && (reinterpret_cast<uintptr_t>(p.w) & 15) == 0;
-  if (p.group_blocks == 0) {
-    const int b0 = blockIdx.x * kAtOnce;
-    float v[kAtOnce][8];
+  const int b0 = static_cast<int>(blockIdx.x % p.units) * kAtOnce;
+  float v[kAtOnce][8];
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) load8(src, (b0 + i) * 128 + l16 * 8, p.cols, fast, v[i]);
+  for (int i = 0; i < kAtOnce; ++i) load8(src, (b0 + i) * 128 + l16 * 8, p.cols, fast, v[i]);
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      const int block = b0 + i, col = block * 128 + l16 * 8;
-      if (block >= p.blocks) break;
-      Extremes<ZERO> e;
-      e.add(v[i]);
-      e.over(p.lanes);
-      const int group = block * (16 / p.lanes) + l16 / p.lanes;
-      const Code c = group_code(p, e, row, group, l16 % p.lanes == 0 && group < p.groups);
-      put_word(p, v[i], c, tile, block, row16, l16, ok, col);
-    }
-  } else {
-    const int group = blockIdx.x;
-    const int b0 = group * p.group_blocks, b1 = min(b0 + p.group_blocks, p.blocks);
-    float v[8];
+  for (int i = 0; i < kAtOnce; ++i) {
+    const int block = b0 + i, col = block * 128 + l16 * 8;
+    if (block >= p.blocks) break;
     Extremes<ZERO> e;
+    e.add(v[i]);
+    e.over(p.lanes);
+    const int group = block * (16 / p.lanes) + l16 / p.lanes;
+    const Code c = group_code(p, e, row, group, l16 % p.lanes == 0 && group < p.groups);
+    put_word(p, v[i], c, tile, block, row16, l16, ok, col);
+  }
+}
+
+// Groups longer than a block: a CTA takes two rows of a group, its warps every
+// kWarps-th block; the extremes meet in shared memory, and the second pass
+// reads the blocks from the cache.
+template <typename T, bool ZERO>
+__global__ void __launch_bounds__(kWarps * 32) int4_quantize_long_kernel(const __grid_constant__ Params p) {
+  __shared__ float hi[kWarps][2], minus_lo[kWarps][2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l16 = lane & 15, half = lane >> 4;
+  const int pair = static_cast<int>(blockIdx.x / p.units), tile = pair >> 3, row16 = (pair & 7) * 2 + half;
+  const int row = tile * 16 + row16;
+  const bool ok = row < p.rows;
+  const T* const src = static_cast<const T*>(p.w) + static_cast<size_t>(ok ? row : p.rows - 1) * p.cols;
+  const bool fast = (p.cols * sizeof(T)) % 16 == 0 && (reinterpret_cast<uintptr_t>(p.w) & 15) == 0;
+  const int group = static_cast<int>(blockIdx.x % p.units);
+  const int b0 = group * p.group_blocks, b1 = min(b0 + p.group_blocks, p.blocks);
+  float v[8];
+  Extremes<ZERO> e;
 #pragma unroll 4
-    for (int block = b0; block < b1; ++block) {
-      load8(src, block * 128 + l16 * 8, p.cols, fast, v);
-      e.add(v);
-    }
-    e.over(16);
-    const Code c = group_code(p, e, row, group, l16 == 0);
+  for (int block = b0 + warp; block < b1; block += kWarps) {
+    load8(src, block * 128 + l16 * 8, p.cols, fast, v);
+    e.add(v);
+  }
+  e.over(16);
+  if (l16 == 0) {
+    hi[warp][half] = e.hi;
+    minus_lo[warp][half] = e.minus_lo;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    e.hi = max_nan(e.hi, hi[w][half]);
+    if (ZERO) e.minus_lo = max_nan(e.minus_lo, minus_lo[w][half]);
+  }
+  const Code c = group_code(p, e, row, group, warp == 0 && l16 == 0);
 #pragma unroll 4
-    for (int block = b0; block < b1; ++block) {
-      const int col = block * 128 + l16 * 8;
-      load8(src, col, p.cols, fast, v);
-      put_word(p, v, c, tile, block, row16, l16, ok, col);
-    }
+  for (int block = b0 + warp; block < b1; block += kWarps) {
+    const int col = block * 128 + l16 * 8;
+    load8(src, col, p.cols, fast, v);
+    put_word(p, v, c, tile, block, row16, l16, ok, col);
   }
 }
 
 template <typename T>
-void launch(const Params& p, cudaStream_t s) {
-  const int units = p.group_blocks ? p.groups : (p.blocks + kAtOnce - 1) / kAtOnce;
-  const dim3 grid(static_cast<unsigned>(units), static_cast<unsigned>((p.rows + 15) / 16));
-  if (p.zeros) int4_quantize_kernel<T, true><<<grid, kWarps * 32, 0, s>>>(p);
-  else int4_quantize_kernel<T, false><<<grid, kWarps * 32, 0, s>>>(p);
+void launch(const Params& p, unsigned grid, cudaStream_t s) {
+  if (p.group_blocks) {
+    if (p.zeros) int4_quantize_long_kernel<T, true><<<grid, kWarps * 32, 0, s>>>(p);
+    else int4_quantize_long_kernel<T, false><<<grid, kWarps * 32, 0, s>>>(p);
+  } else {
+    if (p.zeros) int4_quantize_kernel<T, true><<<grid, kWarps * 32, 0, s>>>(p);
+    else int4_quantize_kernel<T, false><<<grid, kWarps * 32, 0, s>>>(p);
+  }
 }
 
 }  // namespace
@@ -191,8 +215,8 @@ extern "C" bcjr_status bcjr_int4_quantize(const void* w, int w_dtype, int rows, 
                                           bcjr_stream_t stream) {
   if (!dtype_ok(w_dtype) || !dtype_ok(scale_dtype) || rows < 0 || cols < 1 || group_size < 0) return BCJR_ERR_INVALID_ARG;
   if (group_size % 128 != 0 && group_size != 32 && group_size != 64) return BCJR_ERR_UNSUPPORTED;
-  // tiles are the second grid dimension; columns as in the product
-  if (rows > 16 * 65535 || cols > (1 << 27)) return BCJR_ERR_UNSUPPORTED;
+  // columns as in the product
+  if (rows > (1 << 30) || cols > (1 << 27)) return BCJR_ERR_UNSUPPORTED;
   if (rows == 0) return BCJR_OK;
   if (!w || !packed || !scales || !ptr_aligned(w, dtype_size(w_dtype)) || !ptr_aligned(packed, 16) ||
       !ptr_aligned(scales, dtype_size(scale_dtype)))
@@ -217,9 +241,12 @@ extern "C" bcjr_status bcjr_int4_quantize(const void* w, int w_dtype, int rows, 
     p.group_blocks = group_size / 128;
     p.groups = (cols + group_size - 1) / group_size;
   }
+  p.units = static_cast<unsigned>(p.group_blocks ? p.groups : (p.blocks + kAtOnce - 1) / kAtOnce);
+  const long long grid = static_cast<long long>((rows + 15) / 16) * (p.group_blocks ? 8 : 1) * p.units;
+  if (grid > 0x7FFFFFFFll) return BCJR_ERR_UNSUPPORTED;
   cudaStream_t s = as_stream(stream);
-  if (w_dtype == BCJR_F32) launch<float>(p, s);
-  else if (w_dtype == BCJR_F16) launch<__half>(p, s);
-  else launch<__nv_bfloat16>(p, s);
+  if (w_dtype == BCJR_F32) launch<float>(p, static_cast<unsigned>(grid), s);
+  else if (w_dtype == BCJR_F16) launch<__half>(p, static_cast<unsigned>(grid), s);
+  else launch<__nv_bfloat16>(p, static_cast<unsigned>(grid), s);
   return launched();
 }

@@ -12,8 +12,8 @@ extern "C" bcjr_status bcjr_trellis_matmul(const void* x, int x_dtype, int token
       state_bits < 1 || k < 1 || k > state_bits || group_size < 0)
     return BCJR_ERR_INVALID_ARG;
   if (cols % seq_len != 0) return BCJR_ERR_INVALID_ARG;
-  // token passes are the second grid dimension; columns and bits are counted in ints
-  if (k > 4 || state_bits > 16 || tokens > 65535 || rows > (1 << 30) || cols > (1 << 28)) return BCJR_ERR_UNSUPPORTED;
+  // passes of 8 tokens are the second grid dimension; columns and bits are counted in ints
+  if (k > 4 || state_bits > 16 || tokens > 8 * 65535 || rows > (1 << 30) || cols > (1 << 28)) return BCJR_ERR_UNSUPPORTED;
   int group = cols;
   if (scales && group_size > 0) {
     group = group_size;

@@ -23,13 +23,19 @@ _current_device = torch._C._cuda_getDevice
 STATE_BLOCK = 256  # elements of a block of optimiser state
 
 
+_calls = {}
+
+
 def _call(name, index, *args):
     """The library's call `name` on the current stream of device `index`."""
+    call = _calls.get(name)
+    if call is None:
+        call = _calls[name] = getattr(lib(), name)
     if _current_device() == index:
-        status = getattr(lib(), name)(*args, _raw_stream(index))
+        status = call(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            status = getattr(lib(), name)(*args, _raw_stream(index))
+            status = call(*args, _raw_stream(index))
     if status:
         raise BCJRError(status, name)
 
@@ -51,6 +57,18 @@ def _like(t, name, shape, dtype, index):
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+
+
+def _tokens(x):
+    """x [..., cols] as (device index, type code, leading sizes, cols)."""
+    index, kind = x.get_device(), _DTYPE.get(x.dtype)
+    if index < 0 or kind is None or not x.is_contiguous():
+        _on_device(x, "x")
+        _dtype(x, "x")
+    lead = list(x.shape)
+    if not lead or lead[-1] < 1:
+        raise ValueError("x must be [..., cols]")
+    return index, kind, lead, lead.pop()
 
 
 def _dtype(t, name):
@@ -161,12 +179,13 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
         if any(end > start for (_, end), (start, _) in zip(spans, spans[1:])):
             raise ValueError("parameters must not overlap") from None
         raise
-    torch.autograd.graph.increment_version(params)
+    _increment_version(params)
 
 
 _get_device, _is_contiguous, _numel, _data_ptr = (torch.Tensor.get_device, torch.Tensor.is_contiguous, torch.Tensor.numel,
                                                   torch.Tensor.data_ptr)
 _get_dtype = torch.Tensor.dtype.__get__
+_increment_version = torch.autograd.graph.increment_version
 
 
 def _one_dtype(ts, name):
@@ -211,20 +230,15 @@ def int4_matmul(x, packed, scales, zeros=None, group_size=128, out=None):
     """x [..., cols] times the transpose of 4-bit weights: [..., rows] of x's
     type, sums in float32.  `packed`, `scales`, `zeros` and `group_size` as
     `int4_quantize` gives and takes them."""
-    index = _on_device(x, "x")
-    kind = _dtype(x, "x")
-    if x.dim() < 1:
-        raise ValueError("x must be [..., cols]")
-    *lead, cols = x.shape
-    if cols < 1:
-        raise ValueError("x must have columns")
-    if scales.dim() != 2:
+    index, kind, lead, cols = _tokens(x)
+    grouped = scales.shape
+    if len(grouped) != 2 or grouped[0] != _groups(cols, group_size):
         raise ValueError("scales must be [groups][rows]")
-    rows = scales.shape[1]
-    _like(scales, "scales", (_groups(cols, group_size), rows), scales.dtype, index)
-    _like(packed, "packed", (-(-rows // 16), -(-cols // 128), 1024), torch.uint8, index)
+    rows = grouped[1]
+    _like(scales, "scales", grouped, scales.dtype, index)
+    _like(packed, "packed", (rows + 15 >> 4, cols + 127 >> 7, 1024), torch.uint8, index)
     if zeros is not None:
-        _like(zeros, "zeros", scales.shape, torch.uint8, index)
+        _like(zeros, "zeros", grouped, torch.uint8, index)
     lead.append(rows)
     if out is None:
         out = x.new_empty(lead)
@@ -274,13 +288,7 @@ def trellis_matmul(x, packed, codebook, state_bits, k, seq_len, scales=None, gro
     group_size][rows]) when given.  group_size: 0 for one scale a row, a
     multiple of seq_len that divides cols, or a multiple of 16 that divides
     seq_len.  Products and sums are float32."""
-    index = _on_device(x, "x")
-    kind = _dtype(x, "x")
-    if x.dim() < 1:
-        raise ValueError("x must be [..., cols]")
-    *lead, cols = x.shape
-    if cols < 1:
-        raise ValueError("x must have columns")
+    index, kind, lead, cols = _tokens(x)
     if seq_len < 1 or cols % seq_len:
         raise ValueError("a row must be whole sequences")
     seqs = cols // seq_len

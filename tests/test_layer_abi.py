@@ -78,7 +78,7 @@ def test_int4_arguments(lib):
         return q(w, wd, rows, cols, group, packed, scales, sd, zeros, None)
 
     assert quantize(wd=7) == INVALID and quantize(sd=3) == INVALID and quantize(rows=-1) == INVALID and quantize(cols=0) == INVALID
-    assert quantize(group=48) == UNSUPPORTED and quantize(rows=1 << 21) == UNSUPPORTED
+    assert quantize(group=48) == UNSUPPORTED and quantize(rows=(1 << 30) + 1) == UNSUPPORTED
     assert quantize(w=None) == INVALID and quantize(packed=None) == INVALID and quantize(scales=None) == INVALID
     assert quantize(w=4097, wd=1) == INVALID and quantize(packed=8196) == INVALID
     assert quantize(rows=0) == 0
