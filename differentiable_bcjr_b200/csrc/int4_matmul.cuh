@@ -59,6 +59,12 @@ struct Half2<__half> {
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   }
+  // the same onto nothing
+  static __device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  }
 };
 
 template <>
@@ -74,6 +80,12 @@ struct Half2<__nv_bfloat16> {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  }
+  // the same onto nothing
+  static __device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
   }
 };
 
@@ -106,6 +118,16 @@ struct Group {  // of one row
   float scale;
   uint32_t zero;  // what the codes' bits less their zero point start from
 };
+
+// A group's sums, scaled, onto the total: rows g (the first two) and g + 8.
+__device__ __forceinline__ void scaled_add(float (&total)[4], const float (&acc)[4], float lo, float hi) {
+  const float2 a = __ffma2_rn(make_float2(acc[0], acc[1]), make_float2(lo, lo), make_float2(total[0], total[1]));
+  const float2 b = __ffma2_rn(make_float2(acc[2], acc[3]), make_float2(hi, hi), make_float2(total[2], total[3]));
+  total[0] = a.x;
+  total[1] = a.y;
+  total[2] = b.x;
+  total[3] = b.y;
+}
 
 // Bytes of a staged mma column of `blocks` blocks of 128 columns: the odd 64
 // keep the lanes' reads of different columns off one another's banks.
@@ -223,18 +245,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2) int4_matmul_kernel(const __gri
         for (int j = 0; j < 4; ++j) {
           const int f = j * 32 / FLUSH;
           const Group gl = groups[at * NF + f][tile * 16 + g], gh = groups[at * NF + f][tile * 16 + g + 8];
-          if (j * 32 % FLUSH == 0) {
-            acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
-          }
           uint32_t al[4], ah[4];
           H::words(lo[j], gl.zero, magic, al);
           H::words(hi[j], gh.zero, magic, ah);
           const uint4 x = *reinterpret_cast<const uint4*>(xcol + at * 256 + j * 64);
-          H::mma(acc, al[0], ah[0], al[1], ah[1], x.x, x.y);
+          if (j * 32 % FLUSH == 0) H::mma_first(acc, al[0], ah[0], al[1], ah[1], x.x, x.y);
+          else H::mma(acc, al[0], ah[0], al[1], ah[1], x.x, x.y);
           H::mma(acc, al[2], ah[2], al[3], ah[3], x.z, x.w);
           if ((j + 1) * 32 % FLUSH == 0) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) total[tile][c] = fmaf(acc[c], c < 2 ? gl.scale : gh.scale, total[tile][c]);
+            scaled_add(total[tile], acc, gl.scale, gh.scale);
           }
         }
         fetch(slot, base + at + (i % TILES + AHEAD) / TILES * kWarps, (i + AHEAD) % TILES);
@@ -272,7 +291,7 @@ constexpr int kChunk = 8;              // blocks of 128 columns that it stages a
 // NT: tiles of 8 mma columns, for more than 8.  FLUSH: columns after which the sums are scaled
 // (the group, or 128 of a longer one).
 template <typename XT, int NT, int FLUSH>
-__global__ void __launch_bounds__(kRowWarps * 32, NT == 2 ? 3 : 2) int4_matmul_rows_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kRowWarps * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2) int4_matmul_rows_kernel(const __grid_constant__ Params p) {
   constexpr int PARTS = sizeof(XT) == 4 ? 3 : 1;
   constexpr int NF = 128 / FLUSH;  // scalings of a block of 128 columns
   constexpr int AHEAD = 2;         // blocks in flight
@@ -328,25 +347,19 @@ __global__ void __launch_bounds__(kRowWarps * 32, NT == 2 ? 3 : 2) int4_matmul_r
           for (int j = 0; j < 4; ++j) {
             const int f = j * 32 / FLUSH;
             const Group gl = g_lo[((b + i) * NF + f) * kRows], gh = g_lo[((b + i) * NF + f) * kRows + 8];
-            if (j * 32 % FLUSH == 0) {
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
-            }
             uint32_t al[4], ah[4];
             H::words(lo[j], gl.zero, magic, al);
             H::words(hi[j], gh.zero, magic, ah);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const uint4 x = *reinterpret_cast<const uint4*>(xcol[nt] + (b + i) * 256 + j * 64);
-              H::mma(acc[nt], al[0], ah[0], al[1], ah[1], x.x, x.y);
+              if (j * 32 % FLUSH == 0) H::mma_first(acc[nt], al[0], ah[0], al[1], ah[1], x.x, x.y);
+              else H::mma(acc[nt], al[0], ah[0], al[1], ah[1], x.x, x.y);
               H::mma(acc[nt], al[2], ah[2], al[3], ah[3], x.z, x.w);
             }
             if ((j + 1) * 32 % FLUSH == 0) {
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) total[nt][c] = fmaf(acc[nt][c], c < 2 ? gl.scale : gh.scale, total[nt][c]);
-              }
+              for (int nt = 0; nt < NT; ++nt) scaled_add(total[nt], acc[nt], gl.scale, gh.scale);
             }
           }
           if (base + b + i + AHEAD < last) {
@@ -416,11 +429,13 @@ bcjr_status launch_rows(const Params& p, int passes, int sms, cudaStream_t s) {
   const int columns = (p.tokens < p.pass_tokens ? p.tokens : p.pass_tokens) * PARTS;
   const int staged = columns * x_row(kChunk) + kChunk * (128 / FLUSH) * kRows * static_cast<int>(sizeof(Group));
   static_assert(x_row(kChunk) >= (kRows + 4) * 4, "the sums fit where the tokens were");
-  // columns are split over the CTAs of a cluster while the rows alone do not
-  // give every multiprocessor three CTAs
+  // Columns are split over the CTAs of a cluster while the rows alone do not
+  // give every multiprocessor its CTAs: two for 8 columns, which wait for
+  // weights, one for more, which the matrix instruction holds up (8192 x 8192, 32
+  // tokens: 24.1 us with one, 28.0 with two; 8 tokens: 14.9 and 12.8).
   const long long tiles = (p.rows + kRows - 1) / kRows;
   int split = 1;
-  while (split < 8 && tiles * passes * split < 3 * sms && p.blocks >= 2 * split) split *= 2;
+  while (split < 8 && tiles * passes * split < (NT == 1 ? 2 : 1) * sms && p.blocks >= 2 * split) split *= 2;
   auto* const kernel = int4_matmul_rows_kernel<XT, NT, FLUSH>;
   static int most[64];
   if (!allow_shared(reinterpret_cast<const void*>(kernel), most, staged)) return BCJR_ERR_CUDA;
@@ -448,6 +463,10 @@ bcjr_status launch_tokens(Params p, int sms, cudaStream_t s) {
   const int nt = p.tokens * PARTS <= 8 ? 1 : p.tokens * PARTS <= 16 ? 2 : 4;
   p.pass_tokens = nt * 8 / PARTS;
   const int passes = (p.tokens + p.pass_tokens - 1) / p.pass_tokens;
+  // With more than four columns the staged tokens cost the CTAs of few rows more
+  // than their warps save by sharing no sums (8192 x 8192, 8 bf16 tokens: 16.1 us
+  // against 12.8; 3 tokens: 12.6 against 12.5; 1 token of 2048 x 8192: 4.5 against 6.4).
+  if (nt == 1 && p.tokens * PARTS > 4) return launch_rows<XT, 1, FLUSH>(p, passes, sms, s);
   if (nt == 2) return launch_rows<XT, 2, FLUSH>(p, passes, sms, s);
   if (nt == 4) return launch_rows<XT, 4, FLUSH>(p, passes, sms, s);
   // two row tiles a CTA once that leaves every multiprocessor more than one
