@@ -291,7 +291,7 @@ constexpr int kChunk = 8;              // blocks of 128 columns that it stages a
 // NT: tiles of 8 mma columns, for more than 8.  FLUSH: columns after which the sums are scaled
 // (the group, or 128 of a longer one).
 template <typename XT, int NT, int FLUSH>
-__global__ void __launch_bounds__(kRowWarps * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2) int4_matmul_rows_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kRowWarps * 32, NT == 1 ? 4 : 2) int4_matmul_rows_kernel(const __grid_constant__ Params p) {
   constexpr int PARTS = sizeof(XT) == 4 ? 3 : 1;
   constexpr int NF = 128 / FLUSH;  // scalings of a block of 128 columns
   constexpr int AHEAD = 2;         // blocks in flight
