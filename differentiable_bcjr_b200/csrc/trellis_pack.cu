@@ -1,8 +1,8 @@
 // trellis_pack.cu -- hard-decoded states to k bits a weight (bcjr_trellis_pack).
 //
 // The stream of a sequence is the state_bits - k upper bits of its first state
-// and then the low k bits of every state.  A warp takes 32 pieces of 32 states:
-// it loads them piece by piece, coalesced, leaves the low bits as bytes in
+// and then the low k bits of every state.  A warp takes 32 (or 8)
+// pieces of 32 states: it loads them piece by piece, coalesced, leaves the low bits as bytes in
 // shared memory, and then lane l puts the words of piece l together.  What
 // precedes a piece in the stream are the upper bits of its first state, so no
 // piece waits for another.  Reading the states (4 B a weight) bounds the call.
@@ -25,38 +25,40 @@ struct Params {
   long long total;  // pieces of all sequences
 };
 
-template <int K, bool CHECK>
+// PIECES: of a warp; 8 where 32 would leave most of the GPU without a warp.
+template <int K, bool CHECK, int PIECES>
 __global__ void __launch_bounds__(kWarps * 32) trellis_pack_kernel(const __grid_constant__ Params p) {
   __shared__ __align__(4) uint8_t codes[kWarps][32 * kPitch];
   const int lane = threadIdx.x & 31;
   uint8_t* const mine = codes[threadIdx.x >> 5];
-  const long long q0 = (static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * 32;
+  const long long q0 = (static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * PIECES;
   if (q0 >= p.total) return;
-  long long seq = q0 / p.per_seq;
+  // (a division of 64 bits takes as long as a piece)
+  long long seq = p.total <= 0x7FFFFFFFll ? static_cast<uint32_t>(q0) / static_cast<uint32_t>(p.per_seq) : q0 / p.per_seq;
   int piece = static_cast<int>(q0 - seq * p.per_seq);
   // lane l's own piece
-  const long long q = q0 + lane;
-  const long long my_seq = q / p.per_seq;
-  const int my_piece = static_cast<int>(q - my_seq * p.per_seq);
-  const bool have = q < p.total;
+  const int ahead = (piece + lane) / p.per_seq;
+  const long long my_seq = seq + ahead;
+  const int my_piece = piece + lane - ahead * p.per_seq;
+  const bool have = lane < PIECES && q0 + lane < p.total;
   const uint32_t my_first = have ? static_cast<uint32_t>(p.states[my_seq * p.n + 32 * my_piece]) : 0u;
 
   bool bad = false;
-  if (!CHECK && p.dense && q0 + 32 <= p.total) {
+  if (!CHECK && p.dense && q0 + PIECES <= p.total) {
     // whole pieces that follow one another: four states a lane at a time
     const int4* const from = reinterpret_cast<const int4*>(p.states + q0 * 32) + lane;
-    int4 v[8];
+    int4 v[PIECES / 4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __ldcs(from + i * 32);
+    for (int i = 0; i < PIECES / 4; ++i) v[i] = __ldcs(from + i * 32);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < PIECES / 4; ++i) {
       constexpr uint32_t low = (1u << K) - 1u;
       const uint32_t four = (v[i].x & low) | ((v[i].y & low) << 8) | ((v[i].z & low) << 16) | ((v[i].w & low) << 24);
       *reinterpret_cast<uint32_t*>(mine + (i * 4 + (lane >> 3)) * kPitch + (lane & 7) * 4) = four;
     }
   } else
 #pragma unroll 8
-  for (int i = 0; i < 32; ++i) {
+  for (int i = 0; i < PIECES; ++i) {
     uint32_t state = 0;
     if (q0 + i < p.total) {
       const int t = 32 * piece + lane;
@@ -109,11 +111,18 @@ __global__ void __launch_bounds__(kWarps * 32) trellis_pack_kernel(const __grid_
   }
 }
 
-template <int K>
-bcjr_status launch(const Params& p, unsigned grid, cudaStream_t s) {
-  if (p.bad) trellis_pack_kernel<K, true><<<grid, kWarps * 32, 0, s>>>(p);
-  else trellis_pack_kernel<K, false><<<grid, kWarps * 32, 0, s>>>(p);
+template <int K, int PIECES>
+bcjr_status launch_pieces(const Params& p, cudaStream_t s) {
+  const long long grid = (p.total + PIECES * kWarps - 1) / (PIECES * kWarps);
+  if (grid > 0x7FFFFFFFll) return BCJR_ERR_UNSUPPORTED;
+  if (p.bad) trellis_pack_kernel<K, true, PIECES><<<static_cast<unsigned>(grid), kWarps * 32, 0, s>>>(p);
+  else trellis_pack_kernel<K, false, PIECES><<<static_cast<unsigned>(grid), kWarps * 32, 0, s>>>(p);
   return launched();
+}
+
+template <int K>
+bcjr_status launch(const Params& p, int sms, cudaStream_t s) {
+  return p.total < 32ll * kWarps * 2 * sms ? launch_pieces<K, 8>(p, s) : launch_pieces<K, 32>(p, s);
 }
 
 }  // namespace
@@ -136,13 +145,13 @@ extern "C" bcjr_status bcjr_trellis_pack(const int32_t* states, int state_bits, 
   p.per_seq = (seq_len + 31) / 32;
   p.dense = seq_len % 32 == 0 && ptr_aligned(states, 16);
   p.total = static_cast<long long>(p.per_seq) * n_seq;
-  const long long grid = (p.total + 32 * kWarps - 1) / (32 * kWarps);
-  if (grid > 0x7FFFFFFFll) return BCJR_ERR_UNSUPPORTED;
+  const int sms = sm_count();
+  if (sms <= 0) return BCJR_ERR_CUDA;
   cudaStream_t s = as_stream(stream);
   switch (k) {
-    case 1: return launch<1>(p, static_cast<unsigned>(grid), s);
-    case 2: return launch<2>(p, static_cast<unsigned>(grid), s);
-    case 3: return launch<3>(p, static_cast<unsigned>(grid), s);
-    default: return launch<4>(p, static_cast<unsigned>(grid), s);
+    case 1: return launch<1>(p, sms, s);
+    case 2: return launch<2>(p, sms, s);
+    case 3: return launch<3>(p, sms, s);
+    default: return launch<4>(p, sms, s);
   }
 }
