@@ -3,6 +3,9 @@
 // An elementwise pass: every byte of p, g and the two states is read once and
 // p and the states are written once, so memory bandwidth bounds it (28 B an
 // element for float32 with 32-bit states, 10.06 B for bf16 with 8-bit ones).
+// Measured: 16.8 M float32 elements with 32-bit states 73.8 us (6.4 TB/s, 98 %
+// of the copy rate); 134 M bf16 elements with 8-bit states 382 us (3.5 TB/s),
+// held up by issuing some 79 instructions an element.
 // The flat states are cut into blocks of 256 elements, the blocks that 8-bit
 // scales belong to; a warp takes one block at a time, 8 elements a lane, and
 // finds its tensor by bisection in a table that travels as a kernel

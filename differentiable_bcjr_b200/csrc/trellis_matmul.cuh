@@ -19,6 +19,10 @@
 // twice, every state's gather being skipped in the walk that lacks it (half
 // the lanes of a gather meet in fewer banks, so both walks together take less
 // than two full ones).
+//
+// Measured, device time a call: 2048 x 8192, k = 2, 2^16 states, one token 13.5 us
+// with a bf16 codebook (its gathers alone, at 3.5 clocks a warp, would take 6.6 us), 20.4 us
+// with a float32 one; 8192 x 2048, k = 4, bf16 codebook, 8 tokens 21.7 us.
 #pragma once
 #include <type_traits>
 
@@ -347,6 +351,8 @@ bcjr_status launch(Params p, int sms, cudaStream_t s) {
 
 template <int K, Held HELD>
 bcjr_status launch_tokens(const Params& p, int sms, cudaStream_t s) {
+  // 16 columns a lane while their inputs leave registers for the rows' words: one
+  // token 20.4 us (8 columns: 23.8), four 43.7 us (8 columns: 27.0)
   if (p.tokens == 1) return launch<K, 1, 16, HELD>(p, sms, s);
   if (p.tokens <= 4) return launch<K, 4, 8, HELD>(p, sms, s);
   return launch<K, 8, 8, HELD>(p, sms, s);
