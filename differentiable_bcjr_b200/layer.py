@@ -195,6 +195,13 @@ def _one_dtype(ts, name):
     return kinds.pop()
 
 
+def _apart(out, x):
+    """Other rows are still read from x while out is written."""
+    a, b = out.data_ptr(), x.data_ptr()
+    if a < b + x.numel() * x.element_size() and b < a + out.numel() * out.element_size():
+        raise ValueError("out must not overlap x")
+
+
 def _groups(cols, group_size):
     if group_size < 0 or (group_size % 128 and group_size not in (32, 64)):
         raise ValueError("group_size must be 32, 64, a multiple of 128, or 0 for the whole row")
@@ -244,6 +251,7 @@ def int4_matmul(x, packed, scales, zeros=None, group_size=128, out=None):
         out = x.new_empty(lead)
     else:
         _like(out, "out", tuple(lead), x.dtype, index)
+        _apart(out, x)
     _call("bcjr_int4_matmul", index, x.data_ptr(), kind, x.numel() // cols, rows, cols, packed.data_ptr(),
           scales.data_ptr(), _dtype(scales, "scales"), None if zeros is None else zeros.data_ptr(), group_size,
           out.data_ptr())
@@ -308,6 +316,7 @@ def trellis_matmul(x, packed, codebook, state_bits, k, seq_len, scales=None, gro
         out = x.new_empty(lead)
     else:
         _like(out, "out", tuple(lead), x.dtype, index)
+        _apart(out, x)
     _call("bcjr_trellis_matmul", index, x.data_ptr(), kind, x.numel() // cols, rows, cols, packed.data_ptr(),
           codebook.data_ptr(), _dtype(codebook, "codebook"), state_bits, k, seq_len,
           None if scales is None else scales.data_ptr(), group_size, out.data_ptr())

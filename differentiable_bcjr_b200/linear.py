@@ -82,6 +82,9 @@ class TrellisLinear(torch.nn.Module):
     def forward(self, x):
         if x.shape[-1] != self.in_features:
             raise ValueError(f"x must be [..., {self.in_features}]")
-        y = trellis_matmul(_frozen(x), self.packed, self.codebook, self.state_bits, self.k, self.seq_len, self.scales,
+        scales = self.scales  # float32, unless the module was converted as a whole
+        if scales is not None and scales.dtype != torch.float32:
+            scales = scales.float()
+        y = trellis_matmul(_frozen(x), self.packed, self.codebook, self.state_bits, self.k, self.seq_len, scales,
                            self.group_size)
         return y if self.bias is None else y + self.bias

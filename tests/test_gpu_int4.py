@@ -113,6 +113,20 @@ def test_matmul_shapes_views_and_outputs():
     assert B.int4_matmul(x[:0].clone(), packed, scales, zeros, 64).shape == (0, 3, 40)
 
 
+def test_an_output_over_its_input_is_refused():
+    import differentiable_bcjr_b200 as B
+    packed, scales, _ = _layer(256, 256, 64, False, F32, 1)
+    buf = torch.randn(2 * 256 + 5, device="cuda")
+    x = buf[:256].view(1, 256)
+    before = buf.clone()
+    for out in (x, buf[5:261].view(1, 256), buf[255:511].view(1, 256)):
+        with pytest.raises(ValueError):
+            B.int4_matmul(x, packed, scales, None, 64, out=out)
+    assert torch.equal(buf, before)
+    B.int4_matmul(x, packed, scales, None, 64, out=buf[256:512].view(1, 256))
+    assert torch.equal(buf[:256], before[:256]) and torch.equal(buf[512:], before[512:])
+
+
 def test_matmul_of_infinite_and_nan_inputs():
     import differentiable_bcjr_b200 as B
     packed, scales, zeros = _layer(40, 256, 64, False, F32, 2)

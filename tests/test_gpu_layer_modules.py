@@ -157,6 +157,10 @@ def test_trellis_layer_multiplies_what_it_decoded(group, ckind):
     want = x.double() @ used.t()
     size = x.double().abs() @ used.abs().t()
     assert ((y - want).abs() <= size * 64 * 2 ** -24).all()
+    # converted as a whole: codebook and scales lose half a step of the type each, the output one
+    got = layer.half()(x.half()).double()
+    want = x.half().double() @ used.t()
+    assert ((got - want).abs() <= size * 1.01 * (2 ** -11 * 2 + 2 ** -9 * (ckind is not None)) + want.abs() * 2 ** -11 + 2.0 ** -24).all()
 
 
 @pytest.mark.parametrize("optimizer", ["adamw", "adamw8"])

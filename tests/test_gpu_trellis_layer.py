@@ -152,6 +152,7 @@ def test_refusals():
            lambda: B.trellis_matmul(x, packed, c, L, k, n, s, 24),
            lambda: B.trellis_matmul(x, packed, c, L, k, n, s.half(), n),
            lambda: B.trellis_matmul(x, packed, c, L, k, n, out=torch.empty(2, 4, device="cuda")),
+           lambda: B.trellis_matmul(x, packed, c, L, k, n, out=x.view(-1)[100:106].view(2, 3)),
            lambda: B.trellis_pack(packed[0], L, k),
            lambda: B.trellis_pack(packed.float(), L, k),
            lambda: B.trellis_pack(packed.cpu(), L, k),
