@@ -4,8 +4,8 @@
 // p and the states are written once, so memory bandwidth bounds it (28 B an
 // element for float32 with 32-bit states, 10.06 B for bf16 with 8-bit ones).
 // Measured: 16.8 M float32 elements with 32-bit states 73.8 us (6.4 TB/s, 98 %
-// of the copy rate); 134 M bf16 elements with 8-bit states 382 us (3.5 TB/s),
-// held up by issuing some 79 instructions an element.
+// of the copy rate); 134 M bf16 elements with 8-bit states 361 us (3.7 TB/s),
+// held up by issuing some 70 instructions an element, nine of them the hash.
 // The flat states are cut into blocks of 256 elements, the blocks that 8-bit
 // scales belong to; a warp takes one block at a time, 8 elements a lane, and
 // finds its tensor by bisection in a table that travels as a kernel
@@ -110,6 +110,19 @@ __device__ __forceinline__ float rcp_approx(float v) {  // within 2^-23; 0 above
   return r;
 }
 
+// The root of v >= 0 (or NaN), correctly rounded but for a case in millions:
+// y = 1 / sqrt(v) gives g = v y, whose square is v up to a few places, and one
+// Newton step g + (v - g^2) y / 2 with the exact residual of a fused
+// multiply-add.  A few operations without a branch, where __fsqrt_rn takes
+// twice as long here.  0 gives 0; below 2^-126 the root is smaller than it
+// should be; infinity gives a NaN.
+__device__ __forceinline__ float root(float v) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaxf(v, 0x1p-126f)));
+  const float g = __fmul_rn(v, y);
+  return fmaf(fmaf(-g, g, v), 0.5f * y, g);
+}
+
 // Which elements of its block a lane holds: COALESCED 4 at 4 lane and 4 at
 // 128 + 4 lane (16-byte loads of float32); PACKED 8 at 8 lane (16-byte loads
 // of 16-bit types); STRIDED lane, lane + 32, ... one by one, for tensors that
@@ -187,7 +200,7 @@ __device__ __forceinline__ float advance(float& m, float& v, float& r, float g, 
   } else {
     m = __fadd_rn(__fmul_rn(m, s.b1), __fmul_rn(g, s.c1));
     v = __fadd_rn(__fmul_rn(v, s.b2), __fmul_rn(__fmul_rn(g, g), s.c2));
-    r = __fsqrt_rn(v);
+    r = root(v);
   }
   const float step = m * rcp_approx(fmaf(r, s.inv_sqrt_bc2, s.eps));
   return fmaf(-s.lr_bc1, step, p * s.decay);
@@ -285,8 +298,8 @@ __device__ __forceinline__ void block_step8(P* p, const G* g, const Common& c, c
         x = __fmul_rn(x, small);
         y = __fmul_rn(y, small);
       }
-      ua[i] = e4m3_upper(x, ((h >> 8) & 0xFFFF00u) | 0x80u);
-      ub[i] = e4m3_upper(y, ((h << 8) & 0xFFFF00u) | 0x80u);
+      ua[i] = e4m3_upper(x, __byte_perm(h, 0x80u, 0x5324));  // h's upper half between 0 and 0x80
+      ub[i] = e4m3_upper(y, __byte_perm(h, 0x80u, 0x5104));  // and its lower half
       ua[i] = (ua[i] & 0x7FFFFFFFu) | (__float_as_uint(m[i]) & 0x80000000u);
       ub[i] = max(ub[i], min(__float_as_uint(r[i]), least_b));
     }
