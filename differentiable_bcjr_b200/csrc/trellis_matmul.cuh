@@ -238,7 +238,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) trellis_matmul_kernel(const __
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) word[i] = min((bit >> 5) + i, p.words - 1);
         const size_t row_words = static_cast<size_t>(p.seqs) * p.words;
-        const float* const scale = p.scales ? p.scales + static_cast<size_t>(col / p.group) * p.rows : nullptr;
+        // (a lane without a chunk has sums of 0, which an infinite scale would spoil)
+        const float* const scale = p.scales && have ? p.scales + static_cast<size_t>(col / p.group) * p.rows : nullptr;
 
         // GUARDED: a step behind the chunk's end and a state of the other half
         // are left out.  Otherwise they are a product with 0, which is enough
@@ -295,7 +296,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) trellis_matmul_kernel(const __
                   }
                 }
 #pragma unroll
-                for (int m = 0; m < MT; ++m) v[rr * MT + m] = acc.get(m) * now_scale[r8 + rr];
+                for (int m = 0; m < MT; ++m) {
+                  const float sum = acc.get(m);
+                  // (a chunk may have none of its states in this half: nothing times an infinite scale is nothing)
+                  v[rr * MT + m] = HELD == HALVES && sum == 0.f ? 0.f : sum * now_scale[r8 + rr];
+                }
               }
               sum8(v, lane);
               if ((lane & 3) == 0) {

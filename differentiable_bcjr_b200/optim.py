@@ -63,14 +63,18 @@ class AdamW:
                 kinds = {g.dtype for g in grads if g is not None}
                 if not kinds:
                     continue
-                b["step"] += 1
+                if self.capturable:
+                    step = b["step"].add_(1)
+                else:
+                    step = b["step"] + 1
                 first, second, scales = b["state"]
                 for kind in sorted(kinds, key=str):
                     own = grads if len(kinds) == 1 else [g if g is not None and g.dtype == kind else None for g in grads]
                     own = [g if g is None or g.is_contiguous() else g.contiguous() for g in own]
-                    adamw_step(b["params"], own, first, second, b["step"], lr=group["lr"], betas=group["betas"],
+                    adamw_step(b["params"], own, first, second, step, lr=group["lr"], betas=group["betas"],
                                eps=group["eps"], weight_decay=group["weight_decay"], scales=scales,
                                grad_scale=grad_scale, seed=self.seed)
+                b["step"] = step
 
     def zero_grad(self, set_to_none=True):
         for group in self.param_groups:

@@ -92,6 +92,19 @@ def test_matmul_of_non_finite_inputs_and_codewords(L, ckind):
     assert torch.equal(torch.isfinite(y), torch.isfinite(want)) and torch.isfinite(want).any() and not torch.isfinite(y[0, 1])
 
 
+@pytest.mark.parametrize("L", [8, 16])
+def test_matmul_with_an_infinite_scale(L):
+    import differentiable_bcjr_b200 as B
+    k, n, rows = 2, 50, 30
+    packed = B.trellis_pack(R.random_path(rows * 2, n, L, k, 5).cuda(), L, k)
+    c = I.codebook(1 << L).abs().cuda() + 0.1
+    x = torch.rand(2, 2 * n, device="cuda") + 0.1
+    scales = torch.ones(2, rows, device="cuda")
+    scales[0, 3] = scales[1, 4] = float("inf")
+    y = B.trellis_matmul(x, packed, c, L, k, n, scales, n)
+    assert (y[:, 3:5] == float("inf")).all() and torch.isfinite(y[:, :3]).all() and torch.isfinite(y[:, 5:]).all()
+
+
 def test_decode_pack_and_multiply_as_a_program_does():
     import differentiable_bcjr_b200 as B
     L, k, n, rows, cols = 10, 2, 64, 24, 256
