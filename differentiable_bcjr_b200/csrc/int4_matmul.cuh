@@ -184,12 +184,13 @@ __device__ __forceinline__ void stage(const Params& p, unsigned char* xs, int xr
     const size_t row = static_cast<size_t>(min(row0 + at_row, p.rows - 1));
 #pragma unroll 4
     for (int i = tid / ROWS; i < n * NF; i += THREADS / ROWS) {
-      // columns behind the last group are padding: the last group's scale will do
+      // columns behind the last group are padding, whose sums of 0 are scaled by 0
       int group = min(base * NF + i, p.groups - 1);
       if (FLUSH == 128 && p.long_groups) group = __float2int_rz((static_cast<float>(base + i) + 0.5f) * p.inv_group);
       const size_t at = static_cast<size_t>(group) * p.rows + row;
       Group put;
       put.scale = load_as_f32(p.scales, p.scale_dtype, at);
+      if (FLUSH < 128 && base * NF + i >= p.groups) put.scale = 0.f;
       put.zero = Half2<XT>::zero_pair(p.zeros ? p.zeros[at] : 8u);
       groups[i][at_row] = put;
     }

@@ -143,6 +143,22 @@ def test_matmul_of_infinite_and_nan_inputs():
         assert torch.isfinite(y[0]).all() and torch.isfinite(y[3]).all()
 
 
+@pytest.mark.parametrize("tokens", [1, 20])
+@pytest.mark.parametrize("group", [32, 64, 128, 256, 0])
+def test_matmul_with_an_infinite_scale(tokens, group):
+    import differentiable_bcjr_b200 as B
+    # codes above the zero point and positive inputs: an infinite scale gives infinity, also in a short last group
+    packed, scales, zeros = _layer(40, 300, group, True, F32, 2)
+    packed |= 0x88
+    zeros.fill_(1)
+    scales[0, 3] = scales[-1, 7] = float("inf")
+    x = torch.rand(tokens, 300, device="cuda").bfloat16() + 0.5
+    y = B.int4_matmul(x, packed, scales, zeros, group)
+    bad = torch.zeros(40, dtype=torch.bool, device="cuda")
+    bad[3] = bad[7] = True
+    assert (y[:, bad] == float("inf")).all() and torch.isfinite(y[:, ~bad]).all()
+
+
 def test_float32_inputs_are_not_rounded():
     import differentiable_bcjr_b200 as B
     # one column in use: the products of a 24-bit mantissa and a 4-bit code, a single rounding away
