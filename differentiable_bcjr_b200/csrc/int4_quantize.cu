@@ -3,12 +3,13 @@
 // A warp takes two rows of a 128-column block at a time: lane l holds columns
 // 8 (l mod 16) .. + 7 of row l / 16, which are the eight codes of one 32-bit
 // word of the packed tile, so a lane reads 16 or 32 contiguous bytes and
-// writes one word, four blocks' loads ahead of the work on them.  Groups of 32,
+// writes one word, two blocks' loads ahead of the work on them.  Groups of 32,
 // 64 and 128 columns are 4, 8 and 16 neighbouring lanes, their extremes a few
 // shuffles.  Reading w bounds the call (4.5 B a weight for float32 moved in
-// all, 2.5 B for 16-bit types):
-// 2048 x 8192 float32 in groups of 128 takes 16.4 us (4.6 TB/s), in bf16 with
-// one group a row 14.3 us.
+// all, 2.5 B for 16-bit types): 2048 x 8192 float32 in groups of 128 takes 14.9
+// us (5.1 TB/s); 16-bit types have the same work for fewer bytes and take as long
+// (17.6 us), waiting for one another's shuffles and reciprocals.  Persistent CTAs
+// with the next blocks' loads on the way were slower (19.3 us).
 #include <cmath>
 #include <cstring>
 
