@@ -25,7 +25,7 @@ struct Params {
   const void* w;
   int rows, cols, blocks;   // blocks of 128 columns
   int group_blocks;         // of a group; 0: groups shorter than a block
-  int lanes;                // lanes of a group within its block (4, 8 or 16)
+  int lanes_log2;           // of the lanes of a group within its block (4, 8 or 16)
   int groups;
   unsigned units;           // CTAs of a tile's columns
   uint8_t* packed;
@@ -72,8 +72,11 @@ struct Extremes {
       if (ZERO) minus_lo = max_nan(minus_lo, -v[i]);
     }
   }
-  __device__ __forceinline__ void over(int lanes) {
-    for (int d = 1; d < lanes; d <<= 1) {
+  __device__ __forceinline__ void over(int lanes_log2) {
+#pragma unroll
+    for (int step = 0; step < 4; ++step) {
+      if (step >= lanes_log2) break;
+      const int d = 1 << step;
       hi = max_nan(hi, __shfl_xor_sync(~0u, hi, d));
       if (ZERO) minus_lo = max_nan(minus_lo, __shfl_xor_sync(~0u, minus_lo, d));
     }
@@ -166,9 +169,9 @@ __global__ void __launch_bounds__(kWarps * 32) int4_quantize_kernel(const __grid
     if (block >= p.blocks) break;
     Extremes<ZERO> e;
     e.add(v[i]);
-    e.over(p.lanes);
-    const int group = block * (16 / p.lanes) + l16 / p.lanes;
-    const Code c = group_code<ZERO, HALF>(p, e, row, group, l16 % p.lanes == 0 && group < p.groups);
+    e.over(p.lanes_log2);
+    const int group = (block << (4 - p.lanes_log2)) + (l16 >> p.lanes_log2);
+    const Code c = group_code<ZERO, HALF>(p, e, row, group, (l16 & ((1 << p.lanes_log2) - 1)) == 0 && group < p.groups);
     put_word<ZERO, HALF>(p, v[i], c, tile, block, row16, l16, ok, col);
   }
 }
@@ -194,7 +197,7 @@ __global__ void __launch_bounds__(kWarps * 32) int4_quantize_long_kernel(const _
     load8(src, block * 128 + l16 * 8, p.cols, fast, v);
     e.add(v);
   }
-  e.over(16);
+  e.over(4);
   if (l16 == 0) {
     hi[warp][half] = e.hi;
     minus_lo[warp][half] = e.minus_lo;
@@ -254,7 +257,7 @@ extern "C" bcjr_status bcjr_int4_quantize(const void* w, int w_dtype, int rows, 
     p.group_blocks = p.blocks;
     p.groups = 1;
   } else if (group_size <= 128) {
-    p.lanes = group_size / 8;
+    p.lanes_log2 = group_size == 32 ? 2 : group_size == 64 ? 3 : 4;
     p.groups = (cols + group_size - 1) / group_size;
   } else {
     p.group_blocks = group_size / 128;
