@@ -4,8 +4,9 @@
 // p and the states are written once, so memory bandwidth bounds it (28 B an
 // element for float32 with 32-bit states, 10.06 B for bf16 with 8-bit ones).
 // Measured: 16.8 M float32 elements with 32-bit states 73.8 us (6.4 TB/s, 98 %
-// of the copy rate); 134 M bf16 elements with 8-bit states 361 us (3.7 TB/s),
-// held up by issuing some 70 instructions an element, nine of them the hash.
+// of the copy rate); 134 M bf16 elements with 8-bit states 350 us (3.9 TB/s),
+// held up by issuing some 64 instructions an element, nine of them the hash
+// (71 and 361 us without the packed float32 operations on pairs).
 // The flat states are cut into blocks of 256 elements, the blocks that 8-bit
 // scales belong to; a warp takes one block at a time, 8 elements a lane, and
 // finds its tensor by bisection in a table that travels as a kernel
@@ -15,7 +16,6 @@
 #include <cstring>
 #include <memory>
 #include <new>
-#include <type_traits>
 
 #include "layer_util.cuh"
 
@@ -75,15 +75,15 @@ __device__ __forceinline__ uint32_t hash_bits(uint32_t h) {
   return h ^ (h >> 15);
 }
 
-// The code of a magnitude x, scaled so that its block's largest is 448 2^-120:
+// The code of the magnitude of x (a float's bits), scaled so that its block's largest is 448 2^-120:
 // a float's exponent field is then e4m3's, so the code is the float's bits cut
 // after three mantissa bits; the 20 bits that fall away decide the rounding
 // together with `random`, 16 bits and a half.  Sixteen times their sum has the
-// code in its upper byte.  The largest (at most a few places off 448) does not
+// code in its upper byte (a sign bit of x leaves at the top).  The largest (at most a few places off 448) does not
 // round up, since random is at least eight places short of a whole step.
-__device__ __forceinline__ uint32_t e4m3_upper(float x, uint32_t random) {
+__device__ __forceinline__ uint32_t e4m3_upper(uint32_t x, uint32_t random) {
   uint32_t d;  // (a multiply-add, where a shift and an add would load the busier integer pipe)
-  asm("mad.lo.u32 %0, %1, 16, %2;" : "=r"(d) : "r"(__float_as_uint(x)), "r"(random));
+  asm("mad.lo.u32 %0, %1, 16, %2;" : "=r"(d) : "r"(x), "r"(random));
   return d;
 }
 
@@ -110,17 +110,24 @@ __device__ __forceinline__ float rcp_approx(float v) {  // within 2^-23; 0 above
   return r;
 }
 
-// The root of v >= 0 (or NaN), correctly rounded but for a case in millions:
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// Two sums.  Packed ones are contracted with packed products here, whatever
+// rounding is asked for (scales then differ by one place); these are not.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)); }
+
+// The roots of two v >= 0 (or NaN), correctly rounded but for a case in millions:
 // y = 1 / sqrt(v) gives g = v y, whose square is v up to a few places, and one
 // Newton step g + (v - g^2) y / 2 with the exact residual of a fused
 // multiply-add.  A few operations without a branch, where __fsqrt_rn takes
 // twice as long here.  0 gives 0; below 2^-126 the root is smaller than it
 // should be; infinity gives a NaN.
-__device__ __forceinline__ float root(float v) {
-  float y;
-  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaxf(v, 0x1p-126f)));
-  const float g = __fmul_rn(v, y);
-  return fmaf(fmaf(-g, g, v), 0.5f * y, g);
+__device__ __forceinline__ float2 roots(float2 v) {
+  float2 y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(fmaxf(v.x, 0x1p-126f)));
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(fmaxf(v.y, 0x1p-126f)));
+  const float2 g = __fmul2_rn(v, y);
+  return __ffma2_rn(__ffma2_rn(g, g, __fmul2_rn(v, both(-1.f))), __fmul2_rn(y, both(-0.5f)), g);
 }
 
 // Which elements of its block a lane holds: COALESCED 4 at 4 lane and 4 at
@@ -186,24 +193,26 @@ __device__ __forceinline__ void store8(T* base, int lane, int limit, const T (&v
   }
 }
 
-// m, v and p of one element; r = sqrt(v).  8-bit codes are rounded from m and
-// r: there every operation on the way is rounded by itself and correctly, so
-// that a code does not hang on how the compiler contracts products and sums
-// (one code more or less is a sixteenth of the value, far over what the
-// parameter's float32 arithmetic leaves).
-template <int BITS>
-__device__ __forceinline__ float advance(float& m, float& v, float& r, float g, float p, const Scalars& s) {
-  if constexpr (BITS == 32) {
-    m = fmaf(m, s.b1, g * s.c1);
-    v = fmaf(v, s.b2, g * g * s.c2);
-    r = sqrt_approx(v);
-  } else {
-    m = __fadd_rn(__fmul_rn(m, s.b1), __fmul_rn(g, s.c1));
-    v = __fadd_rn(__fmul_rn(v, s.b2), __fmul_rn(__fmul_rn(g, g), s.c2));
-    r = root(v);
-  }
-  const float step = m * rcp_approx(fmaf(r, s.inv_sqrt_bc2, s.eps));
+// m, v and p of one element.
+__device__ __forceinline__ float advance(float& m, float& v, float g, float p, const Scalars& s) {
+  m = fmaf(m, s.b1, g * s.c1);
+  v = fmaf(v, s.b2, g * g * s.c2);
+  const float step = m * rcp_approx(fmaf(sqrt_approx(v), s.inv_sqrt_bc2, s.eps));
   return fmaf(-s.lr_bc1, step, p * s.decay);
+}
+
+// m, r = sqrt(v) and p of two elements.  8-bit codes are rounded from m and r:
+// every operation on the way is rounded by itself and correctly, so that a
+// code does not hang on how the compiler contracts products and sums (one
+// code more or less is a sixteenth of the value, far over what the parameter's
+// float32 arithmetic leaves).
+__device__ __forceinline__ float2 advance2(float2& m, float2& r, float2 g, float2 p, const Scalars& s) {
+  m = add2(__fmul2_rn(m, both(s.b1)), __fmul2_rn(g, both(s.c1)));
+  const float2 v = add2(__fmul2_rn(__fmul2_rn(r, r), both(s.b2)), __fmul2_rn(__fmul2_rn(g, g), both(s.c2)));
+  r = roots(v);
+  const float2 d = __ffma2_rn(r, both(s.inv_sqrt_bc2), both(s.eps));
+  const float2 step = __fmul2_rn(m, make_float2(rcp_approx(d.x), rcp_approx(d.y)));
+  return __ffma2_rn(step, both(-s.lr_bc1), __fmul2_rn(p, both(s.decay)));
 }
 
 // One block of one tensor.  `limit`: elements of the block that exist.
@@ -221,8 +230,7 @@ __device__ __forceinline__ void block_step32(P* p, const G* g, const Common& c, 
   load8<P, MAP>(p, lane, limit, pv);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    float r;
-    pv[i] = from_f32<P>(advance<32>(m[i], v[i], r, __fmul_rn(to_f32(gv[i]), gs), to_f32(pv[i]), s));
+    pv[i] = from_f32<P>(advance(m[i], v[i], __fmul_rn(to_f32(gv[i]), gs), to_f32(pv[i]), s));
   }
   store8<P, MAP>(p, lane, limit, pv);
   store8<float, MAP>(first, lane, MAP == STRIDED ? limit : kBlock, m);
@@ -245,33 +253,41 @@ __device__ __forceinline__ void block_step8(P* p, const G* g, const Common& c, c
   uint32_t wa[2], wb[2];
   memcpy(wa, a, 8);
   memcpy(wb, b, 8);
-  float m[8], r[8];
+  float2 m[4], r[4];
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    m[i / 2] = make_float2(e4m3_small<true>(wa[i >> 2], i & 3), e4m3_small<true>(wa[i >> 2], (i & 3) + 1));
+    r[i / 2] = make_float2(e4m3_small<false>(wb[i >> 2], i & 3), e4m3_small<false>(wb[i >> 2], (i & 3) + 1));
+  }
   // A code is its float times 2^-120; bringing that back and the scale are one
   // product where 2^120 times the scale is a float (a uniform choice: scales
   // of 128 and more stand for moments beyond 2^15).
-  if (sa < 128.f && sb < 128.f) {
-    const float fa = sa * 0x1p120f, fb = sb * 0x1p120f;
+  float fa = sa * 0x1p120f, fb = sb * 0x1p120f;
+  if (!(sa < 128.f && sb < 128.f)) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      m[i] = __fmul_rn(e4m3_small<true>(wa[i >> 2], i & 3), fa);
-      r[i] = __fmul_rn(e4m3_small<false>(wb[i >> 2], i & 3), fb);
+    for (int i = 0; i < 4; ++i) {
+      m[i] = __fmul2_rn(m[i], both(0x1p120f));
+      r[i] = __fmul2_rn(r[i], both(0x1p120f));
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      m[i] = __fmul_rn(__fmul_rn(e4m3_small<true>(wa[i >> 2], i & 3), 0x1p120f), sa);
-      r[i] = __fmul_rn(__fmul_rn(e4m3_small<false>(wb[i >> 2], i & 3), 0x1p120f), sb);
-    }
+    fa = sa;
+    fb = sb;
   }
   // the order of the magnitudes' bits is that of the values, NaN above all
   uint32_t ta = 0, tb = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float v = __fmul_rn(r[i], r[i]);
-    pv[i] = from_f32<P>(advance<8>(m[i], v, r[i], __fmul_rn(to_f32(gv[i]), gs), to_f32(pv[i]), s));
-    if (MAP == STRIDED && element_of<MAP>(lane, i) >= limit) m[i] = r[i] = 0.f;
-    ta = max(ta, __float_as_uint(m[i]) << 1);
-    tb = max(tb, __float_as_uint(r[i]));
+  for (int i = 0; i < 4; ++i) {
+    m[i] = __fmul2_rn(m[i], both(fa));
+    r[i] = __fmul2_rn(r[i], both(fb));
+    const float2 g2 = __fmul2_rn(make_float2(to_f32(gv[2 * i]), to_f32(gv[2 * i + 1])), both(gs));
+    const float2 p2 = advance2(m[i], r[i], g2, make_float2(to_f32(pv[2 * i]), to_f32(pv[2 * i + 1])), s);
+    pv[2 * i] = from_f32<P>(p2.x);
+    pv[2 * i + 1] = from_f32<P>(p2.y);
+    if (MAP == STRIDED) {
+      if (element_of<MAP>(lane, 2 * i) >= limit) m[i].x = r[i].x = 0.f;
+      if (element_of<MAP>(lane, 2 * i + 1) >= limit) m[i].y = r[i].y = 0.f;
+    }
+    ta = max(ta, max(__float_as_uint(m[i].x) << 1, __float_as_uint(m[i].y) << 1));
+    tb = max(tb, max(__float_as_uint(r[i].x), __float_as_uint(r[i].y)));
   }
   store8<P, MAP>(p, lane, limit, pv);
   const float top_a = __uint_as_float(__reduce_max_sync(~0u, ta) >> 1);
@@ -289,23 +305,24 @@ __device__ __forceinline__ void block_step8(P* p, const G* g, const Common& c, c
   }
   uint32_t h0 = (static_cast<uint32_t>(block * kBlock) + element_of<MAP>(lane, 0)) * kHashA + s.mix;
   uint32_t ua[8], ub[8];
-  auto encode = [&](auto scaled_twice) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t h = hash_bits(h0 + static_cast<uint32_t>(element_of<MAP>(0, i) - element_of<MAP>(0, 0)) * kHashA);
-      float x = __fmul_rn(fabsf(m[i]), inv_a), y = __fmul_rn(r[i], inv_b);
-      if (decltype(scaled_twice)::value) {
-        x = __fmul_rn(x, small);
-        y = __fmul_rn(y, small);
-      }
-      ua[i] = e4m3_upper(x, __byte_perm(h, 0x80u, 0x5324));  // h's upper half between 0 and 0x80
-      ub[i] = e4m3_upper(y, __byte_perm(h, 0x80u, 0x5104));  // and its lower half
-      ua[i] = (ua[i] & 0x7FFFFFFFu) | (__float_as_uint(m[i]) & 0x80000000u);
-      ub[i] = max(ub[i], min(__float_as_uint(r[i]), least_b));
+  for (int i = 0; i < 4; ++i) {
+    float2 x = __fmul2_rn(m[i], both(inv_a)), y = __fmul2_rn(r[i], both(inv_b));
+    if (small != 1.f) {
+      x = __fmul2_rn(x, both(small));
+      y = __fmul2_rn(y, both(small));
     }
-  };
-  if (small == 1.f) encode(std::false_type{});
-  else encode(std::true_type{});
+    const uint32_t two[2][4] = {{__float_as_uint(x.x), __float_as_uint(y.x), __float_as_uint(m[i].x), __float_as_uint(r[i].x)},
+                                {__float_as_uint(x.y), __float_as_uint(y.y), __float_as_uint(m[i].y), __float_as_uint(r[i].y)}};
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const uint32_t h = hash_bits(h0 + static_cast<uint32_t>(element_of<MAP>(0, 2 * i + q) - element_of<MAP>(0, 0)) * kHashA);
+      const uint32_t a4 = e4m3_upper(two[q][0], __byte_perm(h, 0x80u, 0x5324));  // h's upper half between 0 and 0x80
+      const uint32_t b4 = e4m3_upper(two[q][1], __byte_perm(h, 0x80u, 0x5104));  // and its lower half
+      ua[2 * i + q] = (a4 & 0x7FFFFFFFu) | (two[q][2] & 0x80000000u);
+      ub[2 * i + q] = max(b4, min(two[q][3], least_b));
+    }
+  }
 #pragma unroll
   for (int i = 0; i < 8; i += 4) {
     wa[i >> 2] = upper_bytes(ua[i], ua[i + 1], ua[i + 2], ua[i + 3]);
