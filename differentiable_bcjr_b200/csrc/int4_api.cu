@@ -30,6 +30,7 @@ extern "C" bcjr_status bcjr_int4_matmul(const void* x, int x_dtype, int tokens, 
   p.cols = cols;
   p.blocks = (cols + 127) / 128;
   p.fast_x = ptr_aligned(x, 16) && (cols * dtype_size(x_dtype)) % 16 == 0;
+  p.fast_groups = rows % 4 == 0 && ptr_aligned(scales, 4 * dtype_size(scale_dtype)) && ptr_aligned(zeros, 4);
   const int group = group_size == 0 || group_size >= cols ? p.blocks * 128 : group_size;
   p.groups = (cols + group - 1) / group;
   p.inv_group = group >= 128 ? 1.f / static_cast<float>(group / 128) : 0.f;

@@ -15,6 +15,7 @@ struct Int4MatmulParams {
   void* y;
   int tokens, rows, cols, blocks;
   bool fast_x;         // x may be read 16 bytes at a time
+  bool fast_groups;    // scales and zero points may be read four rows at a time
   int groups;
   float inv_group;     // 1 / (blocks of a group), for groups of 128 columns and more
   bool long_groups;    // groups of more than 128 columns

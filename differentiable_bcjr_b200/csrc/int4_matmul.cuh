@@ -20,10 +20,10 @@
 // the CTAs of a cluster split the columns of the matrix and add their sums
 // through distributed shared memory in a fixed order.
 //
-// Measured, device time a call: 8192 x 8192 in groups of 128, one bf16 token 11.2 us
-// (33.6 MB: 3.0 TB/s; reading them alone takes 6.4 us from memory with as many
-// threads), 8 tokens 12.8 us, 32 tokens 24 us; 16384 x 8192 in groups of 32, 16 half
-// tokens 35 us.  The integer pipe (masks and shifts) and too few warps to hide
+// Measured, device time a call: 8192 x 8192 in groups of 128, one bf16 token 10.8 us
+// (33.6 MB: 3.1 TB/s; reading them alone takes 6.4 us from memory with as many
+// threads), 8 tokens 12.4 us, 32 tokens 22.4 us; 16384 x 8192 in groups of 32, 16 half
+// tokens 34 us.  The integer pipe (masks and shifts) and too few warps to hide
 // latencies bound it, not the matrix instruction (20 % busy) nor memory.
 #pragma once
 #include <cooperative_groups.h>
@@ -145,15 +145,21 @@ __device__ __forceinline__ void scaled_add(float (&total)[4], const float (&acc)
 __host__ __device__ constexpr int x_row(int blocks) { return blocks * 256 + 64; }
 
 // Stages blocks base .. base + n - 1: the tokens as mma columns `xrow` bytes
-// apart from `xs`, the scales and zero points of ROWS rows as [group][row].
-template <typename XT, int THREADS, int ROWS, int FLUSH>
+// apart from `xs`, the scales and zero points of ROWS rows as [group][row],
+// four rows a thread where they are aligned for it.  MANY tokens divide the
+// threads by a power of two not below the pieces of one; up to four are told
+// apart by comparing.  Both save the division.
+template <typename XT, int THREADS, int ROWS, int FLUSH, bool MANY>
 __device__ __forceinline__ void stage(const Params& p, unsigned char* xs, int xrow, Group (*groups)[ROWS], int base, int n,
                                       int token0, int tokens, int row0) {
   constexpr int PARTS = sizeof(XT) == 4 ? 3 : 1;
   constexpr int NF = 128 / FLUSH;
   const int tid = threadIdx.x;
-  for (int i = tid; i < tokens * n * 16; i += THREADS) {  // 8 columns of a token
-    const int token = i / (n * 16), piece = i - token * (n * 16), col = base * 128 + piece * 8;
+  const int log = MANY ? 36 - __clz(n - 1) : 0, all = MANY ? 1 << log : n * 16;
+  for (int i = tid; i < tokens * all; i += THREADS) {  // 8 columns of a token
+    const int token = MANY ? i >> log : (i >= all) + (i >= 2 * all) + (i >= 3 * all);
+    const int piece = i - token * all, col = base * 128 + piece * 8;
+    if (MANY && piece >= n * 16) continue;
     const XT* const from = static_cast<const XT*>(p.x) + static_cast<size_t>(token0 + token) * p.cols + col;
     unsigned char* const to = xs + token * PARTS * xrow + piece * 16;
     if (PARTS == 1 && p.fast_x && col + 8 <= p.cols) {
@@ -179,18 +185,42 @@ __device__ __forceinline__ void stage(const Params& p, unsigned char* xs, int xr
       for (int q = 0; q < 3; ++q) *reinterpret_cast<uint4*>(to + q * xrow) = make_uint4(out[q][0], out[q][1], out[q][2], out[q][3]);
     }
   }
-  {
+  // columns behind the last group are padding, whose sums of 0 are scaled by 0
+  auto group_of = [&](int i) {
+    if (FLUSH == 128 && p.long_groups) return __float2int_rz((static_cast<float>(base + i) + 0.5f) * p.inv_group);
+    return min(base * NF + i, p.groups - 1);
+  };
+  auto in_use = [&](int i) { return FLUSH == 128 || base * NF + i < p.groups; };
+  // With 64 registers a thread, four rows pay only for long groups (8192 x 8192
+  // in groups of 128, one token: 10.8 us against 11.2; 16384 x 4096 in groups of
+  // 64 with zero points: 13.4 against 13.0).
+  if ((MANY || FLUSH == 128) && p.fast_groups) {
+    const int at_row = tid % (ROWS / 4) * 4;
+    const size_t row = static_cast<size_t>(min(row0 + at_row, p.rows - 4));
+#pragma unroll(MANY ? 4 : 1)
+    for (int i = tid / (ROWS / 4); i < n * NF; i += THREADS / (ROWS / 4)) {
+      const size_t at = static_cast<size_t>(group_of(i)) * p.rows + row;
+      const uint32_t z = p.zeros ? *reinterpret_cast<const uint32_t*>(p.zeros + at) : 0x08080808u;
+      const float4 scale = load4_as_f32(p.scales, p.scale_dtype, at);
+      const float f[4] = {scale.x, scale.y, scale.z, scale.w};
+      uint32_t word[8];
+#pragma unroll
+      for (int o = 0; o < 4; ++o) {
+        word[2 * o] = in_use(i) ? __float_as_uint(f[o]) : 0u;
+        word[2 * o + 1] = Half2<XT>::zero_pair(z >> (8 * o) & 0xFFu);
+      }
+      uint4* const to = reinterpret_cast<uint4*>(&groups[i][at_row]);
+      to[0] = make_uint4(word[0], word[1], word[2], word[3]);
+      to[1] = make_uint4(word[4], word[5], word[6], word[7]);
+    }
+  } else {
     const int at_row = tid & (ROWS - 1);
     const size_t row = static_cast<size_t>(min(row0 + at_row, p.rows - 1));
 #pragma unroll 4
     for (int i = tid / ROWS; i < n * NF; i += THREADS / ROWS) {
-      // columns behind the last group are padding, whose sums of 0 are scaled by 0
-      int group = min(base * NF + i, p.groups - 1);
-      if (FLUSH == 128 && p.long_groups) group = __float2int_rz((static_cast<float>(base + i) + 0.5f) * p.inv_group);
-      const size_t at = static_cast<size_t>(group) * p.rows + row;
+      const size_t at = static_cast<size_t>(group_of(i)) * p.rows + row;
       Group put;
-      put.scale = load_as_f32(p.scales, p.scale_dtype, at);
-      if (FLUSH < 128 && base * NF + i >= p.groups) put.scale = 0.f;
+      put.scale = in_use(i) ? load_as_f32(p.scales, p.scale_dtype, at) : 0.f;
       put.zero = Half2<XT>::zero_pair(p.zeros ? p.zeros[at] : 8u);
       groups[i][at_row] = put;
     }
@@ -240,7 +270,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) int4_matmul_kernel(const __gri
   for (int base = 0; base < p.blocks; base += p.chunk) {
     const int n = min(p.chunk, p.blocks - base);
     if (base != 0) __syncthreads();
-    stage<XT, kWarps * 32, ROWS, FLUSH>(p, xs, xrow, groups, base, n, token0, tokens, row0);
+    stage<XT, kWarps * 32, ROWS, FLUSH, false>(p, xs, xrow, groups, base, n, token0, tokens, row0);
 
     constexpr int TURN = AHEAD > TILES ? AHEAD : TILES;  // tiles of one pass of the unrolled loop
     static_assert(TURN % TILES == 0 && TURN % AHEAD == 0, "whole blocks, whole rings");
@@ -346,7 +376,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, NT == 1 ? 4 : 2) int4_matmul_r
   for (int base = first; base < last; base += kChunk) {
     const int n = min(kChunk, last - base);
     if (base != first) __syncthreads();
-    stage<XT, kRowWarps * 32, kRows, FLUSH>(p, xs, x_row(kChunk), groups, base, n, token0, tokens, row0);
+    stage<XT, kRowWarps * 32, kRows, FLUSH, true>(p, xs, x_row(kChunk), groups, base, n, token0, tokens, row0);
 
 #pragma unroll 1
     for (int b = 0; b < n; b += AHEAD) {

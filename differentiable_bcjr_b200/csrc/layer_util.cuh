@@ -62,6 +62,18 @@ __device__ __forceinline__ float load_as_f32(const void* p, int dtype, size_t i)
   return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
 }
 
+// Elements i .. i + 3, which are aligned together.
+__device__ __forceinline__ float4 load4_as_f32(const void* p, int dtype, size_t i) {
+  if (dtype == BCJR_F32) return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+  const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+  if (dtype == BCJR_F16) {
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w.x)), b = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                     __uint_as_float(w.y & 0xFFFF0000u));
+}
+
 __device__ __forceinline__ void store_from_f32(void* p, int dtype, size_t i, float v) {
   if (dtype == BCJR_F32) static_cast<float*>(p)[i] = v;
   else if (dtype == BCJR_F16) static_cast<__half*>(p)[i] = __float2half_rn(v);

@@ -159,6 +159,23 @@ def test_matmul_with_an_infinite_scale(tokens, group):
     assert (y[:, bad] == float("inf")).all() and torch.isfinite(y[:, ~bad]).all()
 
 
+@pytest.mark.parametrize("tokens", [1, 3, 7, 20, 33])
+@pytest.mark.parametrize("rows,cols,group", [(4, 40, 0), (132, 1100, 128), (20, 2300, 256), (44, 700, 32), (300, 129, 64)])
+@pytest.mark.parametrize("scale", [F32, F16, BF16])
+def test_matmul_of_unaligned_scales(tokens, rows, cols, group, scale):
+    import differentiable_bcjr_b200 as B
+    packed, scales, zeros = _layer(rows, cols, group, True, scale, rows)
+    x = torch.randn(tokens, cols, device="cuda").bfloat16()
+    y = B.int4_matmul(x, packed, scales, zeros, group)
+    want, tol = _tolerance(x, R.int4_weights(packed, scales, zeros, rows, cols, group), group, BF16)
+    assert ((y.double() - want).abs() <= tol).all()
+    # the same values one element behind an aligned address
+    apart = [torch.cat([t.flatten()[:1], t.flatten()])[1:].view(t.shape) for t in (scales, zeros)]
+    assert all(t.data_ptr() % (4 * t.element_size()) for t in apart)
+    assert torch.equal(B.int4_matmul(x, packed, apart[0], apart[1], group), y)
+    assert torch.equal(B.int4_matmul(x, packed, scales, apart[1], group), y)
+
+
 def test_float32_inputs_are_not_rounded():
     import differentiable_bcjr_b200 as B
     # one column in use: the products of a 24-bit mantissa and a 4-bit code, a single rounding away
