@@ -21,6 +21,11 @@ struct TrellisMatmulParams {
   int chunks;       // of a row
   int wide;         // warps that share a row
   int copies_log2;  // of the codebook
+  int unit_chunks;  // chunks of a scale (of a row without scales)
+  int unit_steps;   // of four chunks, of a scale
+  int steps;        // of a row
+  bool padded;      // some chunks have fewer steps, or some fours fewer chunks
+  uint64_t seq_inverse, unit_inverse;  // 2^40 / per_seq and / unit_steps, rounded up
 };
 
 // One translation unit for each number of bits a step.

@@ -20,14 +20,16 @@
 // the lanes of a gather meet in fewer banks, so both walks together take less
 // than two full ones).
 //
-// Measured, device time a call: 2048 x 8192, k = 2, 2^16 states, one token 13.5 us
+// Measured, device time a call: 2048 x 8192, k = 2, 2^16 states, one token 12.3 us
 // with a bf16 codebook (its gathers alone, at 3.5 clocks a warp, would take 6.6 us), 20.4 us
-// with a float32 one; 8192 x 2048, k = 4, bf16 codebook, 8 tokens 21.7 us.
+// with a float32 one.  Several tokens of the codebook's own 16-bit type take the
+// kernel of trellis_mma.cuh.
 #pragma once
 #include <type_traits>
 
 #include "layer_util.cuh"
 #include "trellis_internal.h"
+#include "trellis_mma.cuh"
 
 namespace bcjr {
 namespace {
@@ -208,7 +210,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1) trellis_matmul_kernel(const __
         } else {
           const unsigned char* const from = static_cast<const unsigned char*>(p.codebook) + phase * kHalf;
           if (HELD == HALVES && threadIdx.x == 0) *reinterpret_cast<float*>(smem + kHalf) = 0.f;
-          fine = copy_in<HELD == HALVES ? 4 : 2>(smem, from, HELD == H16 ? 0x7C000000u : 0x7F800000u);
+          // without padding nothing has to be known of 16-bit codewords
+          if (HELD != HALVES && !p.padded && (reinterpret_cast<uintptr_t>(from) & 15) == 0) {
+            const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+#pragma unroll
+            for (int i = threadIdx.x; i < static_cast<int>(kHalf / 16); i += kWarps * 32)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + i * 16), "l"(from + i * 16) : "memory");
+            asm volatile("cp.async.wait_all;" ::: "memory");
+          } else {
+            fine = copy_in<HELD == HALVES ? 4 : 2>(smem, from, HELD == H16 ? 0x7C000000u : 0x7F800000u);
+          }
         }
         all_finite = __syncthreads_and(fine) != 0;
       }
@@ -335,6 +346,7 @@ bcjr_status launch(Params p, int sms, cudaStream_t s) {
   p.per_seq = (p.n + CH - 1) / CH;
   p.chunks = p.seqs * p.per_seq;
   const int tiles = (p.chunks + 31) / 32;
+  p.padded = p.n % CH != 0 || p.chunks % 32 != 0;
   p.wide = 1;
   while (p.wide < kWarps && p.wide < tiles) p.wide *= 2;
   const size_t S = size_t{1} << p.L;
@@ -364,7 +376,8 @@ bcjr_status launch_tokens(const Params& p, int sms, cudaStream_t s) {
 }
 
 template <int K>
-bcjr_status launch_held(const Params& p, int sms, cudaStream_t s) {
+bcjr_status launch_held(Params p, int sms, cudaStream_t s) {
+  if (tokens_mma::plan(p, sms)) return tokens_mma::launch_types<K>(p, sms, s);
   if (p.L < 16) return launch_tokens<K, F32>(p, sms, s);
   if (p.c_dtype == BCJR_F32) return launch_tokens<K, HALVES>(p, sms, s);
   if (p.c_dtype == BCJR_BF16) return launch_tokens<K, B16>(p, sms, s);

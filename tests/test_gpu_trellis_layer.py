@@ -69,6 +69,54 @@ def test_matmul_matches_the_definition(L, k, n, per_row, rows, group, tokens, ki
         _check(y, *_want(x, states, c, scales, group, rows), -(-per_row * -(-n // 16) // 32))
 
 
+# Inputs and codewords of one 16-bit type are summed by the tensor core: exact products, at most 16 added at a time
+# to a float32 sum of 4 instructions, each cutting what lies 2^-23 below its largest term (four times at worst), then
+# the scale, a warp's other columns and 16 warps.  That is no more than the depth of _check counts.
+@pytest.mark.parametrize("L,k,n,per_row,rows,group", [
+    (4, 4, 64, 2, 5, 64), (8, 2, 64, 3, 33, 16), (6, 1, 1, 7, 9, 0), (10, 2, 100, 5, 20, 100), (12, 3, 77, 4, 50, 154), (16, 2, 256, 32, 40, 0),
+    (16, 4, 256, 8, 3000, 256), (16, 1, 40, 1, 3, 0), (16, 3, 512, 2, 17, 128), (15, 3, 33, 20, 1300, 33), (13, 2, 2048, 9, 4, 2048),
+    (9, 4, 17, 300, 6, 0), (14, 1, 256, 4, 700, 512), (1, 1, 48, 2, 8, 48), (11, 2, 16, 1, 20000, 16),
+    (10, 2, 100, 40, 20, 100), (12, 3, 64, 64, 9, 64), (16, 4, 1024, 4, 600, 256)])
+@pytest.mark.parametrize("tokens", [1, 3, 8, 9, 16, 17, 40])
+@pytest.mark.parametrize("kind", [BF16, F16])
+def test_matmul_of_one_16_bit_type(L, k, n, per_row, rows, group, tokens, kind):
+    import differentiable_bcjr_b200 as B
+    states = R.random_path(rows * per_row, n, L, k, L + n).cuda()
+    packed = B.trellis_pack(states, L, k)
+    c = I.codebook(1 << L).to(kind).cuda()
+    cols = per_row * n
+    gen = torch.Generator().manual_seed(3)
+    flat = torch.randn(1 + tokens * cols, generator=gen).to(kind).cuda()
+    x = flat[1:].view(tokens, cols)  # not 16-byte aligned
+    for scales in (None, (0.5 + torch.rand(cols // group if group else 1, rows, generator=gen)).cuda()):
+        y = B.trellis_matmul(x, packed, c, L, k, n, scales, group)
+        _check(y, *_want(x, states, c, scales, group, rows), -(-per_row * -(-n // 16) // 32))
+        assert torch.equal(B.trellis_matmul(x.clone(), packed, c, L, k, n, scales, group), y)
+        moved = torch.cat([c[:1], c])[1:]
+        assert torch.equal(B.trellis_matmul(x, packed, moved, L, k, n, scales, group), y)
+
+
+@pytest.mark.parametrize("L", [8, 16])
+@pytest.mark.parametrize("kind", [BF16, F16])
+@pytest.mark.parametrize("tokens", [3, 11])
+def test_non_finite_values_of_one_16_bit_type(L, kind, tokens):
+    import differentiable_bcjr_b200 as B
+    k, n, rows = 2, 50, 30  # sequences end inside a chunk
+    states = R.random_path(rows * 2, n, L, k, 5).cuda()
+    states[3] = 0  # a path of the codeword that is infinite below
+    packed = B.trellis_pack(states, L, k, check=True)
+    c = I.codebook(1 << L).to(kind).cuda()
+    x = torch.randn(tokens, 2 * n, device="cuda").to(kind)
+    x[1, 60], x[2, 7] = float("inf"), float("nan")
+    for _ in range(2):
+        want, _ = _want(x, states, c, None, 0, rows)
+        y = B.trellis_matmul(x, packed, c, L, k, n).double()
+        assert torch.equal(torch.isnan(y), torch.isnan(want)) and torch.equal(torch.isinf(y), torch.isinf(want))
+        assert torch.equal(y[torch.isinf(y)], want[torch.isinf(want)]) and torch.isfinite(want[0]).any()
+        # the padding behind a sequence's end reads as state 0, whose codeword must not be met there
+        c[0] = float("inf")
+
+
 @pytest.mark.parametrize("L,ckind", [(8, F32), (16, F32), (16, BF16), (16, F16)])
 def test_matmul_of_non_finite_inputs_and_codewords(L, ckind):
     import differentiable_bcjr_b200 as B
