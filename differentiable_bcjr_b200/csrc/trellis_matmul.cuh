@@ -21,7 +21,7 @@
 // than two full ones).
 //
 // Measured, device time a call: 2048 x 8192, k = 2, 2^16 states, one token 12.3 us
-// with a bf16 codebook (its gathers alone, at 3.5 clocks a warp, would take 6.6 us), 20.4 us
+// with a bf16 codebook (its gathers alone, at 3.5 clocks a warp, would take 6.6 us), 18.8 us
 // with a float32 one.  Several tokens of the codebook's own 16-bit type take the
 // kernel of trellis_mma.cuh.
 #pragma once
@@ -210,8 +210,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) trellis_matmul_kernel(const __
         } else {
           const unsigned char* const from = static_cast<const unsigned char*>(p.codebook) + phase * kHalf;
           if (HELD == HALVES && threadIdx.x == 0) *reinterpret_cast<float*>(smem + kHalf) = 0.f;
-          // without padding nothing has to be known of 16-bit codewords
-          if (HELD != HALVES && !p.padded && (reinterpret_cast<uintptr_t>(from) & 15) == 0) {
+          // without padding nothing has to be known of the codewords
+          if (!p.padded && (reinterpret_cast<uintptr_t>(from) & 15) == 0) {
             const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
 #pragma unroll
             for (int i = threadIdx.x; i < static_cast<int>(kHalf / 16); i += kWarps * 32)

@@ -117,6 +117,27 @@ def test_non_finite_values_of_one_16_bit_type(L, kind, tokens):
         c[0] = float("inf")
 
 
+@pytest.mark.parametrize("L", [8, 16])
+@pytest.mark.parametrize("kind,ckind", [(F32, F32), (F32, BF16), (BF16, BF16), (F16, F16)])
+@pytest.mark.parametrize("tokens", [1, 4, 9])
+def test_infinite_codewords_of_whole_chunks(L, kind, ckind, tokens):
+    import differentiable_bcjr_b200 as B
+    k, n, rows = 2, 256, 40  # no padding anywhere
+    states = R.random_path(rows * 2, n, L, k, 5).cuda()
+    states[3] = 0
+    packed = B.trellis_pack(states, L, k, check=True)
+    c = I.codebook(1 << L).to(ckind).cuda()
+    c[0] = float("inf")
+    c[(1 << L) - 1] = -float("inf")
+    x = torch.rand(tokens, 2 * n, device="cuda").to(kind) + 0.5
+    for _ in range(2):
+        want, _ = _want(x, states, c, None, 0, rows)
+        y = B.trellis_matmul(x, packed, c, L, k, n).double()
+        assert torch.equal(torch.isnan(y), torch.isnan(want)) and torch.equal(torch.isinf(y), torch.isinf(want))
+        assert torch.equal(y[torch.isinf(y)], want[torch.isinf(want)]) and not torch.isfinite(y[0, 1])
+        x[0, 300] = float("inf")
+
+
 @pytest.mark.parametrize("L,ckind", [(8, F32), (16, F32), (16, BF16), (16, F16)])
 def test_matmul_of_non_finite_inputs_and_codewords(L, ckind):
     import differentiable_bcjr_b200 as B
