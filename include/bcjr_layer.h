@@ -129,8 +129,9 @@ bcjr_status bcjr_trellis_pack(const int32_t* states, int state_bits, int k, int 
  * scales (float32 [cols / group_size][rows]) may be NULL (group_size is then
  * ignored).  group_size: 0 for one scale a row, a multiple of seq_len that
  * divides cols, or a multiple of 16 that divides seq_len.  x and y of x_dtype,
- * codebook [2^state_bits] of codebook_dtype; products and sums in float32; y must
- * not overlap x.
+ * codebook [2^state_bits] of codebook_dtype; products and sums in float32 (by the
+ * tensor core for several tokens of the codebook's own 16-bit type); y must not
+ * overlap x.
  */
 bcjr_status bcjr_trellis_matmul(const void* x, int x_dtype, int tokens, int rows, int cols,
                                 const uint32_t* packed, const void* codebook, int codebook_dtype,
