@@ -459,8 +459,8 @@ bcjr_status launch(Params p, int passes, cudaStream_t s) {
   constexpr int sums = kWarps * 8 * (ROWS + 4) * static_cast<int>(sizeof(float));
   const int bytes = staged > sums ? staged : sums;
   auto* const kernel = int4_matmul_kernel<XT, FLUSH, TILES>;
-  static int most[64];
-  if (!allow_shared(reinterpret_cast<const void*>(kernel), most, bytes)) return BCJR_ERR_CUDA;
+  static PerDevice done;
+  if (!allow_shared(reinterpret_cast<const void*>(kernel), done)) return BCJR_ERR_CUDA;
   const dim3 grid(static_cast<unsigned>((p.rows + ROWS - 1) / ROWS), 1, static_cast<unsigned>(passes));
   kernel<<<grid, kWarps * 32, static_cast<size_t>(bytes), s>>>(p);
   return launched();
@@ -480,8 +480,8 @@ bcjr_status launch_rows(const Params& p, int passes, int sms, cudaStream_t s) {
   int split = 1;
   while (split < 8 && tiles * passes * split < (NT == 1 ? 2 : 1) * sms && p.blocks >= 2 * split) split *= 2;
   auto* const kernel = int4_matmul_rows_kernel<XT, NT, FLUSH>;
-  static int most[64];
-  if (!allow_shared(reinterpret_cast<const void*>(kernel), most, staged)) return BCJR_ERR_CUDA;
+  static PerDevice done;
+  if (!allow_shared(reinterpret_cast<const void*>(kernel), done)) return BCJR_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * split), 1, static_cast<unsigned>(passes));
   cfg.blockDim = dim3(kRowWarps * 32);

@@ -1,5 +1,6 @@
 // layer_util.cuh -- element types and small helpers of the calls in bcjr_layer.h.
 #pragma once
+#include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -15,30 +16,48 @@ inline size_t dtype_size(int d) { return d == BCJR_F32 ? 4 : 2; }
 inline bcjr_status launched() { return cudaGetLastError() == cudaSuccess ? BCJR_OK : BCJR_ERR_CUDA; }
 inline cudaStream_t as_stream(bcjr_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
-// Multiprocessors of the current device, asked once a device.
-inline int sm_count() {
-  static int known[64] = {};
+// What is asked of each device once.  Several host threads may call at the same
+// time: they would store the same answer, and nothing is stored of a call that failed.
+constexpr int kDevices = 64;
+using PerDevice = std::atomic<int>[kDevices];
+
+inline int current_device() {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  if (known[dev] == 0) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    known[dev] = n;
-  }
-  return known[dev];
+  return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kDevices ? dev : -1;
 }
 
-// Lets a kernel (one `most` a kernel) use up to `bytes` of dynamic shared
-// memory on the current device; asked again only for more.
-inline bool allow_shared(const void* kernel, int (&most)[64], int bytes) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
-  if (bytes <= most[dev]) return true;
+inline int device_attribute(cudaDeviceAttr attr, PerDevice& known, int dev) {
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, attr, dev) != cudaSuccess) return 0;
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+// Multiprocessors of the current device.
+inline int sm_count() {
+  static PerDevice known;
+  const int dev = current_device();
+  return dev < 0 ? 0 : device_attribute(cudaDevAttrMultiProcessorCount, known, dev);
+}
+
+// Lets a kernel (one `done` a kernel) use as much dynamic shared memory on the
+// current device as a CTA can have.  The limit is the kernel's, for all host
+// threads, so it is never set to what one launch needs: a thread with a small
+// launch would lower it between another one's setting and its launch.
+inline bool allow_shared(const void* kernel, PerDevice& done) {
+  static PerDevice most;
+  const int dev = current_device();
+  if (dev < 0) return false;
+  if (done[dev].load(std::memory_order_acquire)) return true;
+  const int bytes = device_attribute(cudaDevAttrMaxSharedMemoryPerBlockOptin, most, dev);
+  if (bytes <= 0) return false;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
     cudaGetLastError();
     return false;
   }
-  most[dev] = bytes;
+  done[dev].store(1, std::memory_order_release);
   return true;
 }
 

@@ -357,8 +357,8 @@ bcjr_status launch(Params p, int sms, cudaStream_t s) {
   const size_t table = HELD == F32 ? S * 4 << p.copies_log2 : HELD == HALVES ? kHalf + 16 : kHalf;
   const size_t smem = (table + 15) / 16 * 16 + sizeof(float) * kWarps * kSums;
   auto* const kernel = trellis_matmul_kernel<K, MT, CH, HELD>;
-  static int most[64];
-  if (!allow_shared(reinterpret_cast<const void*>(kernel), most, static_cast<int>(smem))) return BCJR_ERR_CUDA;
+  static PerDevice done;
+  if (!allow_shared(reinterpret_cast<const void*>(kernel), done)) return BCJR_ERR_CUDA;
   const int teams = kWarps / p.wide;
   const int useful = (p.rows + teams - 1) / teams;
   const dim3 grid(static_cast<unsigned>(useful < sms ? useful : sms), static_cast<unsigned>((p.tokens + MT - 1) / MT));

@@ -307,8 +307,8 @@ bcjr_status launch(Params p, int sms, cudaStream_t s) {
   while (p.wide < kWarps && p.wide < p.steps) p.wide *= 2;
   const int smem = static_cast<int>(kTable) + kWarps * kTiles * SETS * 32 * static_cast<int>(sizeof(float4));
   auto* const kernel = trellis_mma_kernel<K, WORDS, F16, SETS>;
-  static int most[64];
-  if (!allow_shared(reinterpret_cast<const void*>(kernel), most, smem)) return BCJR_ERR_CUDA;
+  static PerDevice done;
+  if (!allow_shared(reinterpret_cast<const void*>(kernel), done)) return BCJR_ERR_CUDA;
   const int teams = kWarps / p.wide, useful = ((p.rows + 7) / 8 + teams - 1) / teams;
   // Few rows: the CTAs of a cluster split the columns (8 tokens of 100 x 8192: 11.2 us
   // with one, 8.8 with two, 8.3 with four, 10.3 with eight).
