@@ -4,7 +4,7 @@
 // p and the states are written once, so memory bandwidth bounds it (28 B an
 // element for float32 with 32-bit states, 10.06 B for bf16 with 8-bit ones).
 // Measured: 16.8 M float32 elements with 32-bit states 73.8 us (6.4 TB/s, 98 %
-// of the copy rate); 134 M bf16 elements with 8-bit states 350 us (3.9 TB/s),
+// of the copy rate); 134 M bf16 elements with 8-bit states 352 us (3.8 TB/s),
 // held up by issuing some 64 instructions an element, nine of them the hash
 // (71 and 361 us without the packed float32 operations on pairs).
 // The flat states are cut into blocks of 256 elements, the blocks that 8-bit
@@ -54,6 +54,7 @@ struct Common {
   const float* grad_scale;
   double lr, beta1, beta2;
   uint32_t seed;
+  bool small_eps;          // a subnormal second moment's root counts beside eps
   Scalars s;
 };
 
@@ -116,18 +117,29 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 // rounding is asked for (scales then differ by one place); these are not.
 __device__ __forceinline__ float2 add2(float2 a, float2 b) { return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)); }
 
-// The roots of two v >= 0 (or NaN), correctly rounded but for a case in millions:
-// y = 1 / sqrt(v) gives g = v y, whose square is v up to a few places, and one
-// Newton step g + (v - g^2) y / 2 with the exact residual of a fused
-// multiply-add.  A few operations without a branch, where __fsqrt_rn takes
-// twice as long here.  0 gives 0; below 2^-126 the root is smaller than it
-// should be; infinity gives a NaN.
+// The roots of two v in [2^-126, 2^128) correctly rounded but for a case in
+// millions: y = 1 / sqrt(v) gives g = v y, whose square is v up to a few places,
+// and one Newton step g + (v - g^2) y / 2 with the exact residual of a fused
+// multiply-add (P. Markstein, "Computation of elementary functions on the IBM
+// RISC System/6000 processor", 1990).  A few operations without a branch, where
+// __fsqrt_rn takes twice as long here.  0 gives 0; another v below 2^-126 a root
+// that is positive but too small (y stops at 2^63), under 2^-62; infinity a NaN.
+// block_step8 looks for what these come to; their blocks take roots_of_all.
 __device__ __forceinline__ float2 roots(float2 v) {
   float2 y;
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(fmaxf(v.x, 0x1p-126f)));
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(fmaxf(v.y, 0x1p-126f)));
   const float2 g = __fmul2_rn(v, y);
   return __ffma2_rn(__ffma2_rn(g, g, __fmul2_rn(v, both(-1.f))), __fmul2_rn(y, both(-0.5f)), g);
+}
+
+// The same for every v: a power of four brings what is below 2^-126 into range, and its root takes it back out.
+__device__ __forceinline__ float2 roots_of_all(float2 v) {
+  const bool sx = v.x < 0x1p-126f, sy = v.y < 0x1p-126f;
+  float2 r = roots(__fmul2_rn(v, make_float2(sx ? 0x1p64f : 1.f, sy ? 0x1p64f : 1.f)));
+  r = __fmul2_rn(r, make_float2(sx ? 0x1p-32f : 1.f, sy ? 0x1p-32f : 1.f));
+  const float inf = __uint_as_float(0x7F800000u);
+  return make_float2(v.x == inf ? inf : r.x, v.y == inf ? inf : r.y);
 }
 
 // Which elements of its block a lane holds: COALESCED 4 at 4 lane and 4 at
@@ -206,10 +218,11 @@ __device__ __forceinline__ float advance(float& m, float& v, float g, float p, c
 // code does not hang on how the compiler contracts products and sums (one
 // code more or less is a sixteenth of the value, far over what the parameter's
 // float32 arithmetic leaves).
+template <bool ALL>
 __device__ __forceinline__ float2 advance2(float2& m, float2& r, float2 g, float2 p, const Scalars& s) {
   m = add2(__fmul2_rn(m, both(s.b1)), __fmul2_rn(g, both(s.c1)));
   const float2 v = add2(__fmul2_rn(__fmul2_rn(r, r), both(s.b2)), __fmul2_rn(__fmul2_rn(g, g), both(s.c2)));
-  r = roots(v);
+  r = ALL ? roots_of_all(v) : roots(v);
   const float2 d = __ffma2_rn(r, both(s.inv_sqrt_bc2), both(s.eps));
   const float2 step = __fmul2_rn(m, make_float2(rcp_approx(d.x), rcp_approx(d.y)));
   return __ffma2_rn(step, both(-s.lr_bc1), __fmul2_rn(p, both(s.decay)));
@@ -237,12 +250,15 @@ __device__ __forceinline__ void block_step32(P* p, const G* g, const Common& c, 
   store8<float, MAP>(second, lane, MAP == STRIDED ? limit : kBlock, v);
 }
 
-template <typename P, typename G, Map MAP>
-__device__ __forceinline__ void block_step8(P* p, const G* g, const Common& c, const Scalars& s, float gs,
+// ALL: for every second moment; otherwise false, and nothing stored, where the
+// block holds one that roots() does not do.
+template <typename P, typename G, Map MAP, bool ALL>
+__device__ __forceinline__ bool block_step8(P* p, const G* g, const Common& c, const Scalars& s, float gs,
                                             size_t block, int lane, int limit) {
   uint8_t* const first = static_cast<uint8_t*>(c.first) + block * kBlock;
   uint8_t* const second = static_cast<uint8_t*>(c.second) + block * kBlock;
   P pv[8];
+  float2 m[4], r[4];
   G gv[8];
   uint8_t a[8], b[8];
   load8<uint8_t, MAP>(first, lane, kBlock, a);
@@ -253,7 +269,6 @@ __device__ __forceinline__ void block_step8(P* p, const G* g, const Common& c, c
   uint32_t wa[2], wb[2];
   memcpy(wa, a, 8);
   memcpy(wb, b, 8);
-  float2 m[4], r[4];
 #pragma unroll
   for (int i = 0; i < 8; i += 2) {
     m[i / 2] = make_float2(e4m3_small<true>(wa[i >> 2], i & 3), e4m3_small<true>(wa[i >> 2], (i & 3) + 1));
@@ -279,7 +294,7 @@ __device__ __forceinline__ void block_step8(P* p, const G* g, const Common& c, c
     m[i] = __fmul2_rn(m[i], both(fa));
     r[i] = __fmul2_rn(r[i], both(fb));
     const float2 g2 = __fmul2_rn(make_float2(to_f32(gv[2 * i]), to_f32(gv[2 * i + 1])), both(gs));
-    const float2 p2 = advance2(m[i], r[i], g2, make_float2(to_f32(pv[2 * i]), to_f32(pv[2 * i + 1])), s);
+    const float2 p2 = advance2<ALL>(m[i], r[i], g2, make_float2(to_f32(pv[2 * i]), to_f32(pv[2 * i + 1])), s);
     pv[2 * i] = from_f32<P>(p2.x);
     pv[2 * i + 1] = from_f32<P>(p2.y);
     if (MAP == STRIDED) {
@@ -289,12 +304,28 @@ __device__ __forceinline__ void block_step8(P* p, const G* g, const Common& c, c
     ta = max(ta, max(__float_as_uint(m[i].x) << 1, __float_as_uint(m[i].y) << 1));
     tb = max(tb, max(__float_as_uint(r[i].x), __float_as_uint(r[i].y)));
   }
+  const uint32_t most_b = __reduce_max_sync(~0u, tb) & 0x7FFFFFFFu;
+  if constexpr (!ALL) {
+    // roots() does not do (uniform, and rare):
+    // - an infinite v, whose root came out as a NaN (as a NaN's does);
+    // - subnormal ones (whose roots are under 2^-63) where they reach codes.  Beside
+    //   a largest root of 2^-45 they have the smallest code whatever they are exactly;
+    // - subnormal ones where they reach parameters, which they do beside a small eps.
+    if (most_b > 0x7F800000u || (most_b != 0 && most_b < __float_as_uint(0x1p-45f))) return false;
+    if (c.small_eps) {
+      bool some = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        some = some || __float_as_uint(r[i].x) - 1u < __float_as_uint(0x1p-62f) || __float_as_uint(r[i].y) - 1u < __float_as_uint(0x1p-62f);
+      if (__any_sync(~0u, some)) return false;
+    }
+  }
   store8<P, MAP>(p, lane, limit, pv);
   const float top_a = __uint_as_float(__reduce_max_sync(~0u, ta) >> 1);
-  const float top_b = __uint_as_float(__reduce_max_sync(~0u, tb) & 0x7FFFFFFFu);
+  const float top_b = __uint_as_float(most_b);
   const bool held_a = !(top_a < kTiny), held_b = !(top_b < kTiny);
   float inv_a = held_a ? __fmul_rn(__frcp_rn(top_a), 448.f) : 0.f, inv_b = held_b ? __fmul_rn(__frcp_rn(top_b), 448.f) : 0.f;
-  const uint32_t least_b = held_b ? 1u << 24 : 0u;  // r > 0 (then it is over 2^-75) does not become 0
+  const uint32_t least_b = held_b ? 1u << 24 : 0u;  // r > 0 (then it is at least 2^-75) does not become 0
   // The factor 2^-120 goes into the reciprocal where that stays a normal float.
   float small = 1.f;
   if (inv_a >= 0x1p-5f && inv_b >= 0x1p-5f) {
@@ -332,17 +363,24 @@ __device__ __forceinline__ void block_step8(P* p, const G* g, const Common& c, c
   memcpy(b, wb, 8);
   if (lane == 0) {
     c.scales[block] = held_a ? __fmul_rn(top_a, 1.f / 448.f) : 0.f;
-    c.scales[c.all_blocks + block] = held_b ? __fmul_rn(top_b, 1.f / 448.f) : 0.f;
+    // an infinite second moment would hold its block's parameters still for good: a NaN shows instead
+    c.scales[c.all_blocks + block] = !held_b ? 0.f : top_b <= 3.402823466e38f ? __fmul_rn(top_b, 1.f / 448.f) : __uint_as_float(0x7FC00000u);
   }
   store8<uint8_t, MAP>(first, lane, MAP == STRIDED ? limit : kBlock, a);
   store8<uint8_t, MAP>(second, lane, MAP == STRIDED ? limit : kBlock, b);
+  return true;
 }
 
+// False: not done (see block_step8).
 template <typename P, typename G, int BITS, Map MAP>
-__device__ __forceinline__ void block_step(P* p, const G* g, const Common& c, const Scalars& s, float gs,
+__device__ __forceinline__ bool block_step(P* p, const G* g, const Common& c, const Scalars& s, float gs,
                                            size_t block, int lane, int limit) {
-  if constexpr (BITS == 32) block_step32<P, G, MAP>(p, g, c, s, gs, block, lane, limit);
-  else block_step8<P, G, MAP>(p, g, c, s, gs, block, lane, limit);
+  if constexpr (BITS == 32) {
+    block_step32<P, G, MAP>(p, g, c, s, gs, block, lane, limit);
+    return true;
+  } else {
+    return block_step8<P, G, MAP, false>(p, g, c, s, gs, block, lane, limit);
+  }
 }
 
 template <typename P, typename G, int BITS, int CAP>
@@ -362,17 +400,17 @@ __global__ void __launch_bounds__(kWarps * 32) adamw_kernel(const __grid_constan
   }
   const float gs = c.grad_scale ? *c.grad_scale : 1.f;
   const int lane = threadIdx.x & 31;
-  int b = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * t.each;
-  const int end = min(b + t.each, t.blocks);
-  if (b >= end) return;
-  int lo = 0, hi = t.n - 1;  // the last tensor that starts at or before b
+  const int b0 = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * t.each, end = min(b0 + t.each, t.blocks);
+  if (b0 >= end) return;
+  int lo = 0, hi = t.n - 1;  // the last tensor that starts at or before b0
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (t.first_block[mid] <= b) lo = mid;
+    if (t.first_block[mid] <= b0) lo = mid;
     else hi = mid - 1;
   }
   constexpr Map FULL = (BITS == 8 && sizeof(P) == 2 && sizeof(G) == 2) ? PACKED : COALESCED;
-  for (; b < end; ++b) {
+  uint32_t left_out = 0;  // which of the warp's blocks (32 at most) are not done
+  for (int b = b0; b < end; ++b) {
     while (lo + 1 < t.n && t.first_block[lo + 1] <= b) ++lo;
     if (!t.g[lo]) continue;
     const int64_t at = static_cast<int64_t>(b - t.first_block[lo]) * kBlock;
@@ -380,10 +418,24 @@ __global__ void __launch_bounds__(kWarps * 32) adamw_kernel(const __grid_constan
     P* const p = static_cast<P*>(t.p[lo]) + at;
     const G* const g = static_cast<const G*>(t.g[lo]) + at;
     const size_t block = c.block0 + b;
+    bool done;
     if (left >= kBlock && ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(g)) & 15) == 0)
-      block_step<P, G, BITS, FULL>(p, g, c, s, gs, block, lane, kBlock);
+      done = block_step<P, G, BITS, FULL>(p, g, c, s, gs, block, lane, kBlock);
     else
-      block_step<P, G, BITS, STRIDED>(p, g, c, s, gs, block, lane, left < kBlock ? static_cast<int>(left) : kBlock);
+      done = block_step<P, G, BITS, STRIDED>(p, g, c, s, gs, block, lane, left < kBlock ? static_cast<int>(left) : kBlock);
+    if (!done) left_out |= 1u << (b - b0);
+  }
+  if constexpr (BITS == 8) {
+    // A loop of its own, which shares registers with the one above: within that
+    // one it costs every block some (80 and more a thread, two layers of bf16 410
+    // us; so 352, and 348 without it).
+    for (; left_out; left_out &= left_out - 1) {
+      const int b = b0 + __ffs(static_cast<int>(left_out)) - 1;
+      for (lo = t.n - 1; t.first_block[lo] > b;) --lo;
+      const int64_t at = static_cast<int64_t>(b - t.first_block[lo]) * kBlock, left = t.numel[lo] - at;
+      block_step8<P, G, STRIDED, true>(static_cast<P*>(t.p[lo]) + at, static_cast<const G*>(t.g[lo]) + at, c, s, gs, c.block0 + b, lane,
+                                       left < kBlock ? static_cast<int>(left) : kBlock);
+    }
   }
 }
 
@@ -401,7 +453,7 @@ bcjr_status launch(const bcjr_adamw_tensor* ts, int n, Common& c, cudaStream_t s
       t.blocks = static_cast<int>(blocks);
       // finding a block's tensor and the step's constants costs as much as some
       // elements do: several blocks a warp once there are enough for all warps
-      t.each = BITS == 8 && blocks >= int64_t{4} * 64 * sms ? 4 : 1;
+      t.each = BITS == 8 && blocks >= int64_t{4} * 64 * sms ? 4 : 1;  // at most 32
       const int64_t per_cta = int64_t{kWarps} * t.each;
       const unsigned grid = static_cast<unsigned>((blocks + per_cta - 1) / per_cta);
       adamw_kernel<P, G, BITS, CAP><<<grid, kWarps * 32, 0, stream>>>(t, c);
@@ -513,6 +565,9 @@ extern "C" bcjr_status bcjr_adamw_step(const bcjr_adamw_tensor* tensors, int n_t
   c.s.c2 = static_cast<float>(1.0 - o->beta2);
   c.s.eps = static_cast<float>(o->eps);
   c.s.decay = static_cast<float>(1.0 - o->lr * o->weight_decay);
+  // a root of a subnormal v is under 2^-63, and its bias correction is largest in the first step; what is left out
+  // beside an eps 2^24 times as large does not show
+  c.small_eps = o->eps < 0x1p-39 / std::sqrt(1.0 - o->beta2);
   if (!o->step_ptr) {
     bias_scalars(o->lr, o->beta1, o->beta2, static_cast<double>(o->step), c.s);
     c.s.mix = mix_of(static_cast<uint32_t>(o->step), o->seed);

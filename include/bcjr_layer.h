@@ -55,8 +55,10 @@ typedef struct {
  *     value of a code is the number it stands for and averages over many
  *     steps keep moving when a step's change is smaller than a code; r > 0
  *     never becomes 0, so that no later update divides by eps alone.
- *     A gradient that is not finite, or whose square is not, makes its block's
- *     scales not finite, and the block's parameters NaN in the next step.
+ *     Where v overflows (gradients beyond 2^63), the step of that element is 0 as
+ *     with 32 bits; its block's scale of r becomes a NaN, and the block's
+ *     parameters with it in the next step.  A gradient that is not finite makes
+ *     its own parameter NaN and both scales of its block not finite.
  * Types: param and grad float32; param f32 with 16-bit grads; 16-bit param
  * with grads of the same type or float32.  Parameters need only the alignment of their
  * type; the states 16 bytes.  Tensors must not overlap.
