@@ -86,19 +86,29 @@ struct Extremes {
 struct Code {
   float inv;
   int zero;
+  bool tiny;  // inv is of 2^64 times the scale
 };
+
+constexpr float kUp = 0x1p64f;
 
 // The group's scale (rounded to its type and stored by one lane) and how to
 // take codes with it.  Multiplying by the reciprocal instead of dividing by
-// the scale differs from the quotient's rounding only next to a tie.
+// the scale differs from the quotient's rounding only next to a tie.  Scales up
+// to 2^-128, whose reciprocals overflow, and weights are taken 2^64 times as large.
 template <bool ZERO, bool HALF>
 __device__ __forceinline__ Code group_code(const Params& p, const Extremes<ZERO>& e, int row, int group, bool writes) {
   float s = ZERO ? __fmul_rn(__fadd_rn(e.hi, e.minus_lo), 1.f / 15.f) : __fmul_rn(e.hi, 1.f / 7.f);
   if (HALF) s = __half2float(__float2half_rn(s));
   else if (p.scale_dtype == BCJR_BF16) s = __bfloat162float(__float2bfloat16_rn(s));
   Code c;
+  float minus_lo = e.minus_lo;
   c.inv = s > 0.f ? __frcp_rn(s) : 0.f;
-  c.zero = ZERO ? static_cast<int>(fminf(fmaxf(rintf(__fmul_rn(e.minus_lo, c.inv)), 0.f), 15.f)) : 8;
+  c.tiny = !HALF && c.inv > 3.402823466e38f;
+  if (c.tiny) {
+    c.inv = __frcp_rn(__fmul_rn(s, kUp));
+    minus_lo = __fmul_rn(minus_lo, kUp);
+  }
+  c.zero = ZERO ? static_cast<int>(fminf(fmaxf(rintf(__fmul_rn(minus_lo, c.inv)), 0.f), 15.f)) : 8;
   if (writes && row < p.rows) {
     const size_t i = static_cast<size_t>(group) * p.rows + row;
     store_from_f32(p.scales, HALF ? BCJR_F16 : p.scale_dtype, i, s);
@@ -111,21 +121,21 @@ __device__ __forceinline__ Code group_code(const Params& p, const Extremes<ZERO>
 // 1.5 2^23 rounds to the nearest integer, ties to even, and leaves it in the
 // low bits (together with an even zero point; an odd one would turn the ties).
 // What can leave 0..15: with zero points, both ends of a range may round up,
-// which makes 16; a subnormal half scale (HALF) may be half of what it stands
-// for, so either end.  0 times an infinity, a NaN, takes some code of a group
-// whose scale says so.
-template <bool ZERO, bool HALF>
-__device__ __forceinline__ void put_word(const Params& p, const float (&v)[8], const Code& c, int tile, int block,
+// which makes 16; a subnormal half scale, or one of the tiny ones, may be half of
+// what it stands for, so either end (LOOSE).  0 times an infinity, a NaN, takes
+// some code of a group whose scale says so.
+template <bool ZERO, bool LOOSE>
+__device__ __forceinline__ void put_codes(const Params& p, const float (&v)[8], const Code& c, int tile, int block,
                                          int row16, int l16, bool row_ok, int col) {
   uint32_t word = 0;
 #pragma unroll
   for (int o = 0; o < 8; ++o) {
     const float t = __fmul_rn(v[o], c.inv);
     uint32_t q;
-    if (ZERO || HALF) {
+    if (ZERO || LOOSE) {
       int i = __float_as_int(__fadd_rn(t, 12582912.f)) - 0x4B400000 + c.zero;
       i = min(i, 15);
-      if (HALF) i = max(i, 0);
+      if (LOOSE) i = max(i, 0);
       q = static_cast<uint32_t>(i);
     } else {
       q = __float_as_uint(__fadd_rn(t, 12582920.f));
@@ -144,6 +154,18 @@ __device__ __forceinline__ void put_word(const Params& p, const float (&v)[8], c
   const size_t at = (static_cast<size_t>(tile) * p.blocks + block) * 1024 + (row16 >> 3) * 512 + (row16 & 7) * 64 +
                     (l16 & 3) * 16 + (l16 >> 2) * 4;
   *reinterpret_cast<uint32_t*>(p.packed + at) = word;
+}
+
+template <bool ZERO, bool HALF>
+__device__ __forceinline__ void put_word(const Params& p, float (&v)[8], const Code& c, int tile, int block, int row16, int l16,
+                                         bool row_ok, int col) {
+  if (!HALF && c.tiny) {
+#pragma unroll
+    for (int o = 0; o < 8; ++o) v[o] = __fmul_rn(v[o], kUp);
+    put_codes<ZERO, true>(p, v, c, tile, block, row16, l16, row_ok, col);
+  } else {
+    put_codes<ZERO, HALF>(p, v, c, tile, block, row16, l16, row_ok, col);
+  }
 }
 
 // Blocks that a thread loads before it works on them: two, 2048 x 8192 float32
