@@ -118,11 +118,18 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
     `grad_scale`, a float32 CUDA tensor of one element, multiplies every
     gradient (clipping or loss scaling without a synchronisation).
     """
+    plan = _adamw_plan(params, grads, exp_avg, exp_avg_sq, step, lr, betas, eps, weight_decay, scales, grad_scale, seed)
+    if plan is not None:
+        _adamw_run(plan)
+
+
+def _adamw_plan(params, grads, exp_avg, exp_avg_sq, step, lr, betas, eps, weight_decay, scales, grad_scale, seed):
+    """The arguments of `adamw_step` checked and laid out for `_adamw_run`; None if there is nothing to do."""
     n = len(params)
     if len(grads) != n:
         raise ValueError(f"{n} parameters and {len(grads)} gradients")
     if n == 0:
-        return
+        return None
     given = [g for g in grads if g is not None]
     both = list(params) + given
     index = params[0].get_device()
@@ -170,12 +177,23 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
     table[0::3] = array("Q", pp)
     table[1::3] = array("Q", gp)
     table[2::3] = array("Q", numel)
+    return (index, table, (_DTYPE[kind], _DTYPE[gkind], bits, exp_avg.data_ptr(), exp_avg_sq.data_ptr(),
+                           None if scales is None else scales.data_ptr(), ctypes.byref(o)), params)
+
+
+def _adamw_check(plan):
+    """Raises if the library refuses the plan's types or hyperparameters (by a call without tensors, which launches nothing)."""
+    index, _, args, _ = plan
+    _call("bcjr_adamw_step", index, None, 0, *args)
+
+
+def _adamw_run(plan):
+    index, table, args, params = plan
     try:
-        _call("bcjr_adamw_step", index, table.buffer_info()[0], n, _DTYPE[kind], _DTYPE[gkind], bits, exp_avg.data_ptr(),
-              exp_avg_sq.data_ptr(), None if scales is None else scales.data_ptr(), ctypes.byref(o))
+        _call("bcjr_adamw_step", index, table.buffer_info()[0], len(params), *args)
     except BCJRError:
-        size = 4 if kind == torch.float32 else 2
-        spans = sorted((a, a + m * size) for a, m in zip(pp, numel) if m)
+        size = 4 if params[0].dtype == torch.float32 else 2
+        spans = sorted((a, a + m * size) for a, m in zip(table[0::3], table[2::3]) if m)
         if any(end > start for (_, end), (start, _) in zip(spans, spans[1:])):
             raise ValueError("parameters must not overlap") from None
         raise

@@ -8,7 +8,8 @@ from __future__ import annotations
 
 import torch
 
-from . import adamw_state, adamw_step
+from . import adamw_state
+from .layer import _adamw_check, _adamw_plan, _adamw_run
 
 
 class AdamW:
@@ -50,31 +51,51 @@ class AdamW:
                 if not t.is_cuda or not t.is_contiguous() or t.dtype not in (torch.float32, torch.float16, torch.bfloat16):
                     raise ValueError("parameters must be contiguous CUDA tensors of float32, float16 or bfloat16")
                 buckets.setdefault((t.device, t.dtype), []).append(t)
+            for ts in buckets.values():
+                spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in ts if t.numel())
+                if any(end > start for (_, end), (start, _) in zip(spans, spans[1:])):
+                    raise ValueError("parameters must not overlap")
             self._buckets.append([{"params": ts, "state": adamw_state(ts, state_bits),
                                    "step": torch.zeros(1, dtype=torch.int64, device=d) if capturable else 0}
                                   for (d, _), ts in buckets.items()])
 
     @torch.no_grad()
     def step(self, grad_scale=None):
-        """One step; `grad_scale` (a float32 CUDA tensor of one element) multiplies every gradient."""
+        """One step; `grad_scale` (a float32 CUDA tensor of one element) multiplies every gradient.
+        All groups are checked before the first launch, so that a step which is refused changes nothing."""
+        todo = []
         for group, buckets in zip(self.param_groups, self._buckets):
             for b in buckets:
                 grads = [p.grad for p in b["params"]]
                 kinds = {g.dtype for g in grads if g is not None}
                 if not kinds:
                     continue
-                if self.capturable:
-                    step = b["step"].add_(1)
-                else:
-                    step = b["step"] + 1
+                step = b["step"] if self.capturable else b["step"] + 1
                 first, second, scales = b["state"]
+                plans = []
                 for kind in sorted(kinds, key=str):
                     own = grads if len(kinds) == 1 else [g if g is not None and g.dtype == kind else None for g in grads]
                     own = [g if g is None or g.is_contiguous() else g.contiguous() for g in own]
-                    adamw_step(b["params"], own, first, second, step, lr=group["lr"], betas=group["betas"],
-                               eps=group["eps"], weight_decay=group["weight_decay"], scales=scales,
-                               grad_scale=grad_scale, seed=self.seed)
-                b["step"] = step
+                    # (the plan holds addresses, so `own` is kept until the launch)
+                    plans.append((_adamw_plan(b["params"], own, first, second, step, group["lr"], group["betas"], group["eps"],
+                                              group["weight_decay"], scales, grad_scale, self.seed), own))
+                todo.append((b, plans))
+        if sum(len(plans) for _, plans in todo) > 1:  # (one launch is refused as a whole anyway)
+            for _, plans in todo:
+                for plan, _ in plans:
+                    _adamw_check(plan)
+        for b, plans in todo:
+            if self.capturable:
+                b["step"].add_(1)
+            try:
+                for plan, _ in plans:
+                    _adamw_run(plan)
+            except Exception:
+                if self.capturable:
+                    b["step"].sub_(1)
+                raise
+            if not self.capturable:
+                b["step"] += 1
 
     def zero_grad(self, set_to_none=True):
         for group in self.param_groups:
