@@ -20,7 +20,8 @@ from __future__ import annotations
 
 import torch
 
-from . import soft_quantize, viterbi_decode
+from . import soft_quantize, trellis_words, viterbi_decode
+from .layer import _groups
 from .linear import Int4Linear, TrellisLinear
 from .optim import AdamW
 
@@ -49,6 +50,11 @@ def layer_reconstruction_qat(W: torch.Tensor, X: torch.Tensor, codebook: torch.T
         raise ValueError("optimizer must be adam, adamw or adamw8")
     if pack and W.shape[1] % seq_len:
         raise ValueError("to be packed, the layer's rows must be whole sequences")
+    # what would only be refused at the end, with the training lost
+    if pack:
+        trellis_words(state_bits, k, seq_len)
+    if int4_group_size is not None:
+        _groups(W.shape[1], int4_group_size)
     V = W.detach().clone().requires_grad_(True)
     cb = codebook.detach().clone().requires_grad_(train_codebook)
     params = [V] + ([cb] if train_codebook else [])
