@@ -281,6 +281,15 @@ def _trellis(state_bits, k):
         raise ValueError("packed trellis codes need 1 <= k <= 4 and k <= state_bits <= 16")
 
 
+def _trellis_groups(cols, seq_len, group_size):
+    if not group_size:
+        return 1
+    if group_size < 0 or not ((group_size % seq_len == 0 and cols % group_size == 0) or
+                              (group_size % 16 == 0 and seq_len % group_size == 0)):
+        raise ValueError("group_size must be 0, a multiple of seq_len that divides cols, or a multiple of 16 that divides seq_len")
+    return cols // group_size
+
+
 def trellis_words(state_bits, k, seq_len):
     """32-bit words that a packed sequence of seq_len states takes."""
     _trellis(state_bits, k)
@@ -325,10 +334,7 @@ def trellis_matmul(x, packed, codebook, state_bits, k, seq_len, scales=None, gro
     _like(packed, "packed", (rows * seqs, words), torch.int32, index)
     _like(codebook, "codebook", (1 << state_bits,), codebook.dtype, index)
     if scales is not None:
-        if group_size and not ((group_size % seq_len == 0 and cols % group_size == 0) or
-                               (group_size % 16 == 0 and group_size > 0 and seq_len % group_size == 0)):
-            raise ValueError("group_size must be 0, a multiple of seq_len that divides cols, or a multiple of 16 that divides seq_len")
-        _like(scales, "scales", (cols // group_size if group_size else 1, rows), torch.float32, index)
+        _like(scales, "scales", (_trellis_groups(cols, seq_len, group_size), rows), torch.float32, index)
     lead.append(rows)
     if out is None:
         out = x.new_empty(lead)

@@ -7,7 +7,8 @@ from __future__ import annotations
 
 import torch
 
-from . import int4_matmul, int4_quantize, trellis_matmul, trellis_pack, viterbi_decode
+from . import int4_matmul, int4_quantize, trellis_matmul, trellis_pack, trellis_words, viterbi_decode
+from .layer import _trellis_groups
 
 
 def _frozen(x):
@@ -66,10 +67,11 @@ class TrellisLinear(torch.nn.Module):
         rows, cols = w.shape
         if cols % seq_len:
             raise ValueError("a row must be whole sequences")
+        trellis_words(state_bits, k, seq_len)  # what the packing refuses is not decoded first
         w = w.detach().contiguous()
         scales = None
         if group_size is not None:
-            parts = w.view(rows, -1, group_size or cols)
+            parts = w.view(rows, _trellis_groups(cols, seq_len, group_size), -1)
             rms = parts.square().mean(2).sqrt()
             rms = torch.where(rms > 0, rms, torch.ones_like(rms))
             w = (parts / rms[:, :, None]).view(rows, cols)

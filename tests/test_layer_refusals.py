@@ -27,3 +27,17 @@ def test_qat_refuses_codes_that_cannot_be_packed_before_it_trains(state_bits, k)
 def test_qat_refuses_rows_that_are_no_sequences_before_it_trains():
     with pytest.raises(ValueError, match="whole sequences"):
         _qat(W=torch.ones(4, 40), pack=True)
+
+
+@pytest.mark.parametrize("group", [24, 48, -32, 128, 8])
+def test_a_trellis_layer_that_could_not_multiply_is_not_made(group):
+    # 96 columns in sequences of 32: 24 and 8 are no multiples of 16, 48 divides no sequence, 128 no row
+    from differentiable_bcjr_b200.linear import TrellisLinear
+    with pytest.raises(ValueError, match="group_size must be"):
+        TrellisLinear.from_weight(torch.ones(4, 96), torch.zeros(1 << L), L, K, N, group)
+
+
+def test_a_trellis_layer_that_could_not_be_packed_is_not_decoded():
+    from differentiable_bcjr_b200.linear import TrellisLinear
+    with pytest.raises(ValueError, match="packed trellis codes need"):
+        TrellisLinear.from_weight(torch.ones(4, 96), torch.zeros(1 << L), L, 5, N)
