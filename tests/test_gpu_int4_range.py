@@ -74,3 +74,42 @@ def test_subnormal_half_scales(zero, kind, group):
 @pytest.mark.parametrize("scale", [F32, BF16])
 def test_huge_groups(zero, scale):
     _check(_rows_of_all_sizes(96, F32, 100, 126), 32, zero, scale)
+
+
+@pytest.mark.parametrize("tokens", [1, 2, 3, 7, 12])
+@pytest.mark.parametrize("group", [32, 64, 128, 256, 0])
+@pytest.mark.parametrize("rows", [40, 5000])
+def test_float32_tokens_under_an_infinite_scale(tokens, group, rows):
+    import differentiable_bcjr_b200 as B
+    # float32 tokens are multiplied in parts, some of them zero: 0 times infinity must not reach the sum
+    cols = 300
+    gen = torch.Generator().manual_seed(tokens)
+    groups = -(-cols // group) if group else 1
+    packed = (torch.randint(0, 256, (-(-rows // 16), 3, 1024), generator=gen, dtype=torch.uint8) | 0x88).cuda()  # codes 8..15
+    scales = (0.004 + 0.01 * torch.rand(groups, rows, generator=gen)).cuda()
+    zeros = torch.ones(groups, rows, dtype=torch.uint8, device="cuda")
+    scales[0, 3] = scales[-1, 7] = float("inf")
+    scales[groups // 2, 11] = float("nan")
+    x = torch.rand(tokens, cols, generator=gen).cuda() + 0.5
+    x[0] = 1.0  # one part holds all of it
+    x[-1] = x[-1].neg().half().float() if tokens > 1 else x[-1]  # two parts do
+    want = x.double() @ R.int4_weights(packed, scales, zeros, rows, cols, group).t()
+    y = B.int4_matmul(x, packed, scales, zeros, group).double()
+    assert torch.isinf(want[:, [3, 7]]).all() and torch.isnan(want[:, 11]).all()
+    assert torch.equal(torch.isnan(y), torch.isnan(want)) and torch.equal(torch.isinf(y), torch.isinf(want))
+    assert torch.equal(y[torch.isinf(y)], want[torch.isinf(want)])
+    fine = torch.isfinite(want)
+    # positive codes and tokens of one sign: the size of the sum is the sum
+    assert ((y[fine] - want[fine]).abs() <= want[fine].abs() * 64 * 2 ** -23).all()
+
+
+@pytest.mark.parametrize("tokens", [1, 4, 9])
+def test_nan_tokens_of_every_payload(tokens):
+    import differentiable_bcjr_b200 as B
+    packed = torch.full((1, 2, 1024), 0x99, dtype=torch.uint8, device="cuda")  # codes 9: ones
+    x = torch.ones(tokens, 256, device="cuda")
+    for bits in (0x7F800001, 0x7FC00000, 0x7F80FFFF, 0x7F810000, -1):
+        x.view(torch.int32)[-1, 77] = bits
+        for s in (1.0, float("inf")):
+            y = B.int4_matmul(x, packed, torch.full((1, 16), s, device="cuda"), None, 0)
+            assert torch.isnan(y[-1]).all() and (y[:-1] == 256 * s).all()
