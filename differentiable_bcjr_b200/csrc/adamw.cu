@@ -563,7 +563,9 @@ extern "C" bcjr_status bcjr_adamw_step(const bcjr_adamw_tensor* tensors, int n_t
   c.s.c1 = static_cast<float>(1.0 - o->beta1);
   c.s.b2 = static_cast<float>(o->beta2);
   c.s.c2 = static_cast<float>(1.0 - o->beta2);
-  c.s.eps = static_cast<float>(o->eps);
+  // a subnormal denominator's approximate reciprocal is infinite, and 0 times it a NaN; beside the root of a v > 0
+  // (2^-75 at least) what is added here does not show
+  c.s.eps = o->eps > 0 && o->eps < 0x1p-126 ? 0x1p-126f : static_cast<float>(o->eps);
   c.s.decay = static_cast<float>(1.0 - o->lr * o->weight_decay);
   // a root of a subnormal v is under 2^-63, and its bias correction is largest in the first step; what is left out
   // beside an eps 2^24 times as large does not show

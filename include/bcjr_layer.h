@@ -40,7 +40,9 @@ typedef struct {
  * One AdamW step of n_tensors tensors (`tensors` is a HOST array):
  *   g' = g * grad_scale,  m = b1 m + (1 - b1) g',  v = b2 v + (1 - b2) g'^2,
  *   p = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps),
- * computed in float32 and p rounded once to its type.
+ * computed in float32 and p rounded once to its type.  An eps between 0 and
+ * 2^-126 counts as 2^-126; with eps 0 an element whose v is 0 becomes a NaN, as
+ * 0 / 0 does.
  *
  * The states of all tensors lie in one flat array each, tensor i starting at
  * element 256 * sum_{j < i} ceil(numel_j / 256); what lies between a tensor's

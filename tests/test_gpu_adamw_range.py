@@ -151,3 +151,24 @@ def test_codes_of_every_size(size, kind):
             near = ((threshold - 1).abs() <= 16 * 2.0 ** -18) | (part < 2.0 ** -14) | (part > 1 - 2.0 ** -14)
             assert ((got.abs() == want.clamp(max=448)) | near).all()
     assert torch.isfinite(p).all()
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("eps", [1e-37, 1e-38, 1e-40, 1e-45, 1e-60, 5e-324])
+def test_an_eps_below_float32s_normal_numbers(bits, eps):
+    import differentiable_bcjr_b200 as B
+    p = torch.ones(600, device="cuda")
+    first, second, scales = B.adamw_state([p], bits)
+    m = v = torch.zeros(600, dtype=torch.float64, device="cuda")
+    for step in (1, 2):
+        g = torch.linspace(-1, 1, 600, device="cuda")
+        g[::3] = 0  # moments of 0: a step of 0 / eps
+        before = p.clone()
+        if bits == 8:
+            m, r = (t[:600] for t in _states(first, second, scales))
+            v = r * r
+        B.adamw_step([p], [g], first, second, step, 0.25, (0.9, 0.99), eps, scales=scales)
+        want, m, v = R.adamw(before, g, m, v, step, 0.25, 0.9, 0.99, eps, 0.0)
+        assert (p[::3] == 1).all()
+        # a step is at most 0.25 / sqrt(1 - beta2), of ten roundings; the parameter one more
+        assert ((p.double() - want).abs() <= 2.5 * 2 ** -20 + want.abs() * 2 ** -23).all()
