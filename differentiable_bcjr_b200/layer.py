@@ -178,17 +178,18 @@ def _adamw_plan(params, grads, exp_avg, exp_avg_sq, step, lr, betas, eps, weight
     table[1::3] = array("Q", gp)
     table[2::3] = array("Q", numel)
     return (index, table, (_DTYPE[kind], _DTYPE[gkind], bits, exp_avg.data_ptr(), exp_avg_sq.data_ptr(),
-                           None if scales is None else scales.data_ptr(), ctypes.byref(o)), params)
+                           None if scales is None else scales.data_ptr(), ctypes.byref(o)),
+            params, params if len(given) == n else [p for p, g in zip(params, grads) if g is not None])
 
 
 def _adamw_check(plan):
     """Raises if the library refuses the plan's types or hyperparameters (by a call without tensors, which launches nothing)."""
-    index, _, args, _ = plan
+    index, _, args, _, _ = plan
     _call("bcjr_adamw_step", index, None, 0, *args)
 
 
 def _adamw_run(plan):
-    index, table, args, params = plan
+    index, table, args, params, moved = plan
     try:
         _call("bcjr_adamw_step", index, table.buffer_info()[0], len(params), *args)
     except BCJRError:
@@ -197,7 +198,7 @@ def _adamw_run(plan):
         if any(end > start for (_, end), (start, _) in zip(spans, spans[1:])):
             raise ValueError("parameters must not overlap") from None
         raise
-    _increment_version(params)
+    _increment_version(moved)
 
 
 _get_device, _is_contiguous, _numel, _data_ptr = (torch.Tensor.get_device, torch.Tensor.is_contiguous, torch.Tensor.numel,
