@@ -6,7 +6,8 @@ packed weights.
 As in the rest of the binding, tensors must be contiguous CUDA tensors of one
 device, every call is asynchronous on that device's current stream, malformed
 arguments raise before anything is launched, and nothing falls back to
-PyTorch.  The products have no gradient: they serve frozen layers.
+PyTorch.  The products have no gradient: they serve frozen layers, and refuse
+tensors that want one (outside torch.no_grad()).
 """
 from __future__ import annotations
 
@@ -221,6 +222,21 @@ def _apart(out, x):
         raise ValueError("out must not overlap x")
 
 
+def _into(out, shape, x, index, name):
+    """Checks an output of the caller's."""
+    _like(out, "out", tuple(shape), x.dtype, index)
+    _apart(out, x)
+    if out.requires_grad:
+        _no_gradient(name)
+    return out
+
+
+def _no_gradient(name):
+    """For a call of which some tensor wants a gradient."""
+    if torch.is_grad_enabled():
+        raise RuntimeError(f"{name} has no gradient: call it under torch.no_grad(), or with detached tensors")
+
+
 def _groups(cols, group_size):
     if group_size < 0 or (group_size % 128 and group_size not in (32, 64)):
         raise ValueError("group_size must be 32, 64, a multiple of 128, or 0 for the whole row")
@@ -261,20 +277,22 @@ def int4_matmul(x, packed, scales, zeros=None, group_size=128, out=None):
     if len(grouped) != 2 or grouped[0] != _groups(cols, group_size):
         raise ValueError("scales must be [groups][rows]")
     rows = grouped[1]
-    _like(scales, "scales", grouped, scales.dtype, index)
+    if scales.get_device() != index or not scales.is_contiguous():
+        _like(scales, "scales", grouped, scales.dtype, index)
     _like(packed, "packed", (rows + 15 >> 4, cols + 127 >> 7, 1024), torch.uint8, index)
     if zeros is not None:
         _like(zeros, "zeros", grouped, torch.uint8, index)
     lead.append(rows)
+    if x.requires_grad or scales.requires_grad:
+        _no_gradient("int4_matmul")
     if out is None:
-        out = x.new_empty(lead)
+        y = x.new_empty(lead)
     else:
-        _like(out, "out", tuple(lead), x.dtype, index)
-        _apart(out, x)
+        y = _into(out, lead, x, index, "int4_matmul")
     _call("bcjr_int4_matmul", index, x.data_ptr(), kind, x.numel() // cols, rows, cols, packed.data_ptr(),
           scales.data_ptr(), _dtype(scales, "scales"), None if zeros is None else zeros.data_ptr(), group_size,
-          out.data_ptr())
-    return out
+          y.data_ptr())
+    return y
 
 
 def _trellis(state_bits, k):
@@ -333,16 +351,18 @@ def trellis_matmul(x, packed, codebook, state_bits, k, seq_len, scales=None, gro
         raise ValueError("packed must be [rows * cols / seq_len][words]")
     rows = packed.shape[0] // seqs
     _like(packed, "packed", (rows * seqs, words), torch.int32, index)
-    _like(codebook, "codebook", (1 << state_bits,), codebook.dtype, index)
+    if codebook.get_device() != index or not codebook.is_contiguous() or codebook.shape != (1 << state_bits,):
+        _like(codebook, "codebook", (1 << state_bits,), codebook.dtype, index)
     if scales is not None:
         _like(scales, "scales", (_trellis_groups(cols, seq_len, group_size), rows), torch.float32, index)
     lead.append(rows)
+    if x.requires_grad or codebook.requires_grad or (scales is not None and scales.requires_grad):
+        _no_gradient("trellis_matmul")
     if out is None:
-        out = x.new_empty(lead)
+        y = x.new_empty(lead)
     else:
-        _like(out, "out", tuple(lead), x.dtype, index)
-        _apart(out, x)
+        y = _into(out, lead, x, index, "trellis_matmul")
     _call("bcjr_trellis_matmul", index, x.data_ptr(), kind, x.numel() // cols, rows, cols, packed.data_ptr(),
           codebook.data_ptr(), _dtype(codebook, "codebook"), state_bits, k, seq_len,
-          None if scales is None else scales.data_ptr(), group_size, out.data_ptr())
-    return out
+          None if scales is None else scales.data_ptr(), group_size, y.data_ptr())
+    return y
