@@ -292,6 +292,8 @@ def int4_matmul(x, packed, scales, zeros=None, group_size=128, out=None):
     _call("bcjr_int4_matmul", index, x.data_ptr(), kind, x.numel() // cols, rows, cols, packed.data_ptr(),
           scales.data_ptr(), _dtype(scales, "scales"), None if zeros is None else zeros.data_ptr(), group_size,
           y.data_ptr())
+    if out is not None:
+        _increment_version(out)
     return y
 
 
@@ -365,4 +367,6 @@ def trellis_matmul(x, packed, codebook, state_bits, k, seq_len, scales=None, gro
     _call("bcjr_trellis_matmul", index, x.data_ptr(), kind, x.numel() // cols, rows, cols, packed.data_ptr(),
           codebook.data_ptr(), _dtype(codebook, "codebook"), state_bits, k, seq_len,
           None if scales is None else scales.data_ptr(), group_size, y.data_ptr())
+    if out is not None:
+        _increment_version(out)
     return y

@@ -53,3 +53,13 @@ def test_products_do_not_drop_a_gradient_silently():
         with torch.inference_mode():
             assert torch.equal(f(live), want)
 
+
+def test_an_output_that_autograd_has_saved_is_missed():
+    for f, _ in _products():
+        x = torch.randn(3, 128, device="cuda")
+        out = torch.ones(3, 40, device="cuda")
+        a = torch.ones(3, 40, device="cuda", requires_grad=True)
+        y = (a * out).sum()
+        f(x, out=out)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
