@@ -548,6 +548,24 @@ extern "C" bcjr_status bcjr_adamw_step(const bcjr_adamw_tensor* tensors, int n_t
   if ((state_bits == 8) != (scales != nullptr) || !ptr_aligned(scales, 4) || !ptr_aligned(o->grad_scale, 4) ||
       !ptr_aligned(o->step_ptr, 8))
     return BCJR_ERR_INVALID_ARG;
+  {
+    // nor may the states share memory with one another, a parameter or a gradient
+    auto span = [](const void* p, int64_t bytes) {
+      const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+      return Span{at, p ? at + static_cast<uintptr_t>(bytes) : at};
+    };
+    auto meet = [](const Span& a, const Span& b) { return a.begin < b.end && b.begin < a.end; };
+    const int64_t bytes = blocks * kBlock * (state_bits / 8);
+    const Span s[3] = {span(first, bytes), span(second, bytes), span(scales, blocks * 8)};
+    if (meet(s[0], s[1]) || meet(s[0], s[2]) || meet(s[1], s[2])) return BCJR_ERR_INVALID_ARG;
+    for (int i = 0; i < n_tensors; ++i) {
+      if (tensors[i].numel == 0) continue;
+      const Span p = span(tensors[i].param, tensors[i].numel * static_cast<int64_t>(dtype_size(param_dtype)));
+      const Span g = span(tensors[i].grad, tensors[i].numel * static_cast<int64_t>(dtype_size(grad_dtype)));
+      for (const Span& state : s)
+        if (meet(state, p) || meet(state, g)) return BCJR_ERR_INVALID_ARG;
+    }
+  }
   Common c = {};
   c.first = first;
   c.second = second;

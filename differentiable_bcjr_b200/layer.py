@@ -111,7 +111,8 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
     starts at the next multiple of 256 elements): float32, or float8_e4m3fn
     codes with `scales` float32 [2][blocks].  With 8-bit states `exp_avg_sq`
     holds the root of the second moment, and codes are rounded stochastically
-    from a hash of `seed`, the step and the element's index.
+    from a hash of `seed`, the step and the element's index.  The library
+    refuses states that share memory with one another, a parameter or a gradient.
 
     `step` counts from 1; it is a number, or an int64 CUDA tensor of one
     element that the kernel reads (what a captured graph needs: with a number,

@@ -63,7 +63,8 @@ typedef struct {
  *     its own parameter NaN and both scales of its block not finite.
  * Types: param and grad float32; param f32 with 16-bit grads; 16-bit param
  * with grads of the same type or float32.  Parameters need only the alignment of their
- * type; the states 16 bytes.  Tensors must not overlap.
+ * type; the states 16 bytes.  Parameters must not overlap one another, nor the
+ * states one another, a parameter or a gradient.
  */
 bcjr_status bcjr_adamw_step(const bcjr_adamw_tensor* tensors, int n_tensors, int param_dtype,
                             int grad_dtype, int state_bits, void* first, void* second,
