@@ -216,17 +216,15 @@ def _one_dtype(ts, name):
     return kinds.pop()
 
 
-def _apart(out, x):
-    """Other rows are still read from x while out is written."""
-    a, b = out.data_ptr(), x.data_ptr()
-    if a < b + x.numel() * x.element_size() and b < a + out.numel() * out.element_size():
-        raise ValueError("out must not overlap x")
-
-
-def _into(out, shape, x, index, name):
-    """Checks an output of the caller's."""
+def _into(out, shape, x, index, name, weights):
+    """Checks an output of the caller's, into which nothing may be written that is still read for other rows."""
     _like(out, "out", tuple(shape), x.dtype, index)
-    _apart(out, x)
+    a = out.data_ptr()
+    for what, t in (("x", x), *weights):
+        if t is not None:
+            b = t.data_ptr()
+            if a < b + t.numel() * t.element_size() and b < a + out.numel() * out.element_size():
+                raise ValueError(f"out must not overlap {what}")
     if out.requires_grad:
         _no_gradient(name)
     return out
@@ -289,7 +287,7 @@ def int4_matmul(x, packed, scales, zeros=None, group_size=128, out=None):
     if out is None:
         y = x.new_empty(lead)
     else:
-        y = _into(out, lead, x, index, "int4_matmul")
+        y = _into(out, lead, x, index, "int4_matmul", (("packed", packed), ("scales", scales), ("zeros", zeros)))
     _call("bcjr_int4_matmul", index, x.data_ptr(), kind, x.numel() // cols, rows, cols, packed.data_ptr(),
           scales.data_ptr(), _dtype(scales, "scales"), None if zeros is None else zeros.data_ptr(), group_size,
           y.data_ptr())
@@ -364,7 +362,7 @@ def trellis_matmul(x, packed, codebook, state_bits, k, seq_len, scales=None, gro
     if out is None:
         y = x.new_empty(lead)
     else:
-        y = _into(out, lead, x, index, "trellis_matmul")
+        y = _into(out, lead, x, index, "trellis_matmul", (("packed", packed), ("codebook", codebook), ("scales", scales)))
     _call("bcjr_trellis_matmul", index, x.data_ptr(), kind, x.numel() // cols, rows, cols, packed.data_ptr(),
           codebook.data_ptr(), _dtype(codebook, "codebook"), state_bits, k, seq_len,
           None if scales is None else scales.data_ptr(), group_size, y.data_ptr())

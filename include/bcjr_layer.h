@@ -104,7 +104,7 @@ bcjr_status bcjr_int4_quantize(const void* w, int w_dtype, int rows, int cols, i
  * y [tokens][rows] = x [tokens][cols] times the transpose of the 4-bit weights;
  * x and y of x_dtype, sums in float32.  float32 x is multiplied exactly (three
  * bf16 parts).  packed must be 16-byte aligned, x and y to their type, and y must
- * not overlap x.  The weights are read once for every 32 tokens (10 for float32 x).
+ * not overlap any of the others.  The weights are read once for every 32 tokens (10 for float32 x).
  */
 bcjr_status bcjr_int4_matmul(const void* x, int x_dtype, int tokens, int rows, int cols,
                              const void* packed, const void* scales, int scale_dtype,
@@ -136,7 +136,7 @@ bcjr_status bcjr_trellis_pack(const int32_t* states, int state_bits, int k, int 
  * divides cols, or a multiple of 16 that divides seq_len.  x and y of x_dtype,
  * codebook [2^state_bits] of codebook_dtype; products and sums in float32 (by the
  * tensor core for several tokens of the codebook's own 16-bit type); y must not
- * overlap x.
+ * overlap any of the others.
  */
 bcjr_status bcjr_trellis_matmul(const void* x, int x_dtype, int tokens, int rows, int cols,
                                 const uint32_t* packed, const void* codebook, int codebook_dtype,

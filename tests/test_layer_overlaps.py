@@ -2,6 +2,7 @@
 import ctypes
 
 import pytest
+import torch
 
 P, I = ctypes.c_void_p, ctypes.c_int
 INVALID = 1
@@ -40,3 +41,44 @@ def test_states_of_an_adamw_step(bits):
         assert call(scales=(1 << 17) - 28) == INVALID  # 2 x 4 scales of 4 bytes
     two = ((1 << 20, 2 << 20, 600), (3 << 20, 2 << 20, 10))  # (a gradient of two parameters is read only)
     assert call(tensors=two, first=3 << 20) == INVALID and call(tensors=two, second=(3 << 20) + 32) == INVALID
+
+
+class Fake(torch.Tensor):
+    """A CPU tensor that says it is on the first GPU."""
+
+    def get_device(self):
+        return 0
+
+
+def test_outputs_of_the_products(monkeypatch):
+    import differentiable_bcjr_b200 as B
+    from differentiable_bcjr_b200 import layer
+    calls = []
+    monkeypatch.setattr(layer, "_call", lambda *a: calls.append(a[0]))
+
+    def fake(t):
+        return t.as_subclass(Fake)
+
+    # all in one buffer, one after the other: an output may touch but not cover any of them
+    buf = torch.zeros(1 << 16)
+    x, out = fake(buf[:256].view(2, 128)), fake(buf[4096:4096 + 32].view(2, 16))
+    scales, packed = fake(buf[1024:1040].view(1, 16)), fake(buf[2048:2304].view(torch.uint8).view(1, 1, 1024))
+    zeros = fake(buf[1536:1540].view(torch.uint8).view(1, 16))
+    stream, codebook = fake(buf[3072:3072 + 16 * 9].view(torch.int32).view(16, 9)), fake(buf[8192:8192 + 256])
+
+    def int4(out):
+        return B.int4_matmul(x, packed, scales, zeros, 0, out=out)
+
+    def trellis(out):
+        return B.trellis_matmul(x, stream, codebook, 8, 2, 128, scales, 0, out=out)
+
+    for f, others in ((int4, (x, packed, scales, zeros)), (trellis, (x, stream, codebook, scales))):
+        assert f(out) is out
+        for t in others:
+            at = (t.data_ptr() - buf.data_ptr()) // 4
+            end = at + t.numel() * t.element_size() // 4
+            for start in (at, end - 1, max(0, at - 31)):
+                with pytest.raises(ValueError, match="must not overlap"):
+                    f(fake(buf[start:start + 32].view(2, 16)))
+            f(fake(buf[end:end + 32].view(2, 16)))
+    assert calls and set(calls) == {"bcjr_int4_matmul", "bcjr_trellis_matmul"}
