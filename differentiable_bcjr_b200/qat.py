@@ -33,7 +33,7 @@ def _recon_mse(X, W_ref, W_q):
 def layer_reconstruction_qat(W: torch.Tensor, X: torch.Tensor, codebook: torch.Tensor, state_bits: int, k: int,
                              seq_len: int, temperatures, steps_per_temperature: int = 10, lr: float = 0.02,
                              train_codebook: bool = False, optimizer: str = "adam", pack: bool = False,
-                             int4_group_size: int | None = None):
+                             int4_group_size: int | None = None, pack_codebook_dtype: torch.dtype | None = None):
     """Returns a dict with the loss history, the hard-decoded reconstruction MSE
     after QAT (`mse_qat`), that of decoding W directly (`mse_ptq`), and the
     quantised weights.
@@ -41,7 +41,9 @@ def layer_reconstruction_qat(W: torch.Tensor, X: torch.Tensor, codebook: torch.T
     optimizer: "adam" is torch.optim.Adam; "adamw" and "adamw8" are the
     library's fused step (without weight decay, the same update) with moments
     in 32 and 8 bits.  pack: the result also holds `linear`, the trained layer
-    packed at k bits a weight (rows must be whole sequences).  int4_group_size:
+    packed at k bits a weight (rows must be whole sequences), with its codebook
+    in `pack_codebook_dtype` (as it was trained if None; in a 16-bit type,
+    several tokens of that type go through the tensor core).  int4_group_size:
     it also holds `mse_int4`, the error of rounding W to 4 bits in groups of
     that many columns."""
     if W.numel() % seq_len:
@@ -53,6 +55,8 @@ def layer_reconstruction_qat(W: torch.Tensor, X: torch.Tensor, codebook: torch.T
     # what would only be refused at the end, with the training lost
     if pack:
         trellis_words(state_bits, k, seq_len)
+        if pack_codebook_dtype not in (None, torch.float32, torch.float16, torch.bfloat16):
+            raise ValueError(f"pack_codebook_dtype must be float32, float16 or bfloat16, not {pack_codebook_dtype}: no layer keeps such a codebook")
     if int4_group_size is not None:
         _groups(W.shape[1], int4_group_size)
     V = W.detach().clone().requires_grad_(True)
@@ -81,7 +85,7 @@ def layer_reconstruction_qat(W: torch.Tensor, X: torch.Tensor, codebook: torch.T
         result = {"history": [float(h) for h in history], "mse_qat": mse_qat, "mse_ptq": mse_ptq,
                   "w_qat": w_qat, "w_ptq": w_ptq, "preimage": V.detach(), "codebook": cb.detach()}
         if pack:
-            result["linear"] = TrellisLinear.from_weight(V, cb.detach(), state_bits, k, seq_len)
+            result["linear"] = TrellisLinear.from_weight(V, cb.detach(), state_bits, k, seq_len, codebook_dtype=pack_codebook_dtype)
         if int4_group_size is not None:
             int4 = Int4Linear.from_weight(W, int4_group_size)
             result["mse_int4"] = float(((X @ W.T - int4(X.contiguous())) ** 2).mean())
