@@ -17,6 +17,12 @@ def _frozen(x):
     return x.contiguous()
 
 
+def check_codebook_dtype(dtype):
+    """Raises if a layer cannot keep its codebook in `dtype` (None: as it is)."""
+    if dtype not in (None, torch.float32, torch.float16, torch.bfloat16):
+        raise ValueError(f"a layer keeps its codebook in float32, float16 or bfloat16, not {dtype}")
+
+
 class Int4Linear(torch.nn.Module):
     """y = x W^T + bias with W in 4 bits (see `int4_quantize` for the forms).
 
@@ -67,7 +73,9 @@ class TrellisLinear(torch.nn.Module):
         rows, cols = w.shape
         if cols % seq_len:
             raise ValueError("a row must be whole sequences")
-        trellis_words(state_bits, k, seq_len)  # what the packing refuses is not decoded first
+        # what the packing or the product refuses is not decoded first
+        trellis_words(state_bits, k, seq_len)
+        check_codebook_dtype(codebook_dtype)
         w = w.detach().contiguous()
         scales = None
         if group_size is not None:

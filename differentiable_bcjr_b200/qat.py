@@ -22,7 +22,7 @@ import torch
 
 from . import soft_quantize, trellis_words, viterbi_decode
 from .layer import _groups
-from .linear import Int4Linear, TrellisLinear
+from .linear import Int4Linear, TrellisLinear, check_codebook_dtype
 from .optim import AdamW
 
 
@@ -55,8 +55,7 @@ def layer_reconstruction_qat(W: torch.Tensor, X: torch.Tensor, codebook: torch.T
     # what would only be refused at the end, with the training lost
     if pack:
         trellis_words(state_bits, k, seq_len)
-        if pack_codebook_dtype not in (None, torch.float32, torch.float16, torch.bfloat16):
-            raise ValueError(f"pack_codebook_dtype must be float32, float16 or bfloat16, not {pack_codebook_dtype}: no layer keeps such a codebook")
+        check_codebook_dtype(pack_codebook_dtype)
     if int4_group_size is not None:
         _groups(W.shape[1], int4_group_size)
     V = W.detach().clone().requires_grad_(True)

@@ -41,3 +41,10 @@ def test_a_trellis_layer_that_could_not_be_packed_is_not_decoded():
     from differentiable_bcjr_b200.linear import TrellisLinear
     with pytest.raises(ValueError, match="packed trellis codes need"):
         TrellisLinear.from_weight(torch.ones(4, 96), torch.zeros(1 << L), L, 5, N)
+
+
+@pytest.mark.parametrize("kind", [torch.float64, torch.int8])
+def test_a_trellis_layer_of_a_codebook_that_no_product_takes_is_not_made(kind):
+    from differentiable_bcjr_b200.linear import TrellisLinear
+    with pytest.raises(ValueError, match="codebook"):
+        TrellisLinear.from_weight(torch.ones(4, 96), torch.zeros(1 << L), L, K, N, codebook_dtype=kind)
