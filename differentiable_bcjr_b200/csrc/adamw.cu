@@ -68,7 +68,8 @@ __host__ __device__ inline void bias_scalars(double lr, double b1, double b2, do
 }
 
 // 32 bits a (step, seed, element), 16 for either rounding: a multiply and
-// xor-shift mix of h = element * kHashA + mix_of(step, seed).
+// xor-shift mix of h = element * kHashA + mix_of(step, seed); multipliers and
+// shifts of C. Wellons, "Prospecting for Hash Functions", 2018.
 constexpr uint32_t kHashA = 0x9E3779B1u;
 __device__ __forceinline__ uint32_t hash_bits(uint32_t h) {
   h = (h ^ (h >> 15)) * 0x2C1B3C6Du;
