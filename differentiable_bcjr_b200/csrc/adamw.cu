@@ -559,12 +559,15 @@ extern "C" bcjr_status bcjr_adamw_step(const bcjr_adamw_tensor* tensors, int n_t
     const int64_t bytes = blocks * kBlock * (state_bits / 8);
     const Span s[3] = {span(first, bytes), span(second, bytes), span(scales, blocks * 8)};
     if (meet(s[0], s[1]) || meet(s[0], s[2]) || meet(s[1], s[2])) return BCJR_ERR_INVALID_ARG;
+    const Span all = {std::min({s[0].begin, s[1].begin, scales ? s[2].begin : s[1].begin}), std::max({s[0].end, s[1].end, s[2].end})};
+    const uintptr_t p_size = dtype_size(param_dtype), g_size = dtype_size(grad_dtype);
     for (int i = 0; i < n_tensors; ++i) {
-      if (tensors[i].numel == 0) continue;
-      const Span p = span(tensors[i].param, tensors[i].numel * static_cast<int64_t>(dtype_size(param_dtype)));
-      const Span g = span(tensors[i].grad, tensors[i].numel * static_cast<int64_t>(dtype_size(grad_dtype)));
+      const uintptr_t n = static_cast<uintptr_t>(tensors[i].numel);
+      const uintptr_t p_at = reinterpret_cast<uintptr_t>(tensors[i].param), g_at = reinterpret_cast<uintptr_t>(tensors[i].grad);
+      const Span p = {p_at, p_at + n * p_size}, g = {g_at, g_at + n * g_size};
+      if (n == 0 || (!meet(all, p) && !meet(all, g))) continue;
       for (const Span& state : s)
-        if (meet(state, p) || meet(state, g)) return BCJR_ERR_INVALID_ARG;
+        if (meet(state, p) || (g_at && meet(state, g))) return BCJR_ERR_INVALID_ARG;
     }
   }
   Common c = {};
