@@ -8,7 +8,8 @@
 // is exactly 128 + q, and one packed subtraction gives q - zero, exactly.
 // Group sums stay in float32 and are scaled in float32, so the only rounding
 // is that of the sums.  float32 tokens are cut into three bf16 parts of 8
-// bits (exact), which take three of the eight columns.
+// bits (exact, the lower ones held 2^8 and 2^16 times as large), which take three
+// of the eight columns.
 //
 // Global loads return in the order they were issued, so inputs and scales are
 // staged in shared memory first and only the weights, two tiles ahead, are
@@ -103,24 +104,31 @@ struct Half2<__nv_bfloat16> {
 template <>
 struct Half2<float> : Half2<__nv_bfloat16> {};
 
-// A float as three bf16's bits: the upper 8 bits of its mantissa, the next 8,
-// the last 8, each cut off exactly.  An infinity is its own first part and
-// leaves 0 for the others; a NaN, also one of the lowest bits alone, has one there.
+// A float as three bf16's bits: the upper 8 bits of its mantissa, the next 8
+// times 2^8, the last 8 times 2^16, each cut off exactly (where they are they may
+// lie below bf16's smallest number, 2^-133).  An infinity is its own first part
+// and leaves 0 for the others; a NaN, also one of the lowest bits alone, has one there.
+constexpr float kPart = 0x1p8f, kPartDown = 0x1p-8f;
+__device__ __forceinline__ bool finite(float v) { return fabsf(v) <= 3.402823466e38f; }
 __device__ __forceinline__ void parts_of(float v, uint32_t (&out)[3]) {
   const float top = __uint_as_float((v == v ? __float_as_uint(v) : 0x7FFF0000u) & 0xFFFF0000u);
-  const float rest = top == v ? 0.f : v - top;
+  const float rest = top == v ? 0.f : __fmul_rn(v - top, kPart);
   const float mid = __uint_as_float(__float_as_uint(rest) & 0xFFFF0000u);
-  const float low = mid == rest ? 0.f : rest - mid;
+  const float low = __fmul_rn(rest - mid, kPart);
   out[0] = __float_as_uint(top) >> 16;
   out[1] = __float_as_uint(mid) >> 16;
   out[2] = __float_as_uint(low) >> 16;
 }
 
-// A sum over the lower parts of values: what is not finite comes with the first
-// part, and a lower part's 0 times an infinite scale is a NaN that the value has
-// not.  (Asked where sums are written: asked where the CTAs' sums are added it
-// keeps their loads from running ahead, 4.9 us a call for 4.6.)
-__device__ __forceinline__ float lower_parts(float v) { return fabsf(v) <= 3.402823466e38f ? v : 0.f; }
+// A sum over values or over one of their parts, of mma column `column`, as it
+// counts in the values' sum.  What is not finite comes with the first part: a
+// lower part's 0 times an infinite scale is a NaN that the value has not.  (Done
+// where sums are written: where they are added up it keeps their loads from
+// running ahead, 4.9 us a call for 4.5.)
+template <int PARTS>
+__device__ __forceinline__ float part_sum(float v, int column) {
+  return column % PARTS == 0 ? v : (finite(v) ? v : 0.f) * (column % PARTS == 1 ? kPartDown : kPartDown * kPartDown);
+}
 
 // Weights are read once: they would only push the inputs out of the L1 cache.
 __device__ __forceinline__ uint4 load_once(const uint4* p) {
@@ -173,8 +181,16 @@ __device__ __forceinline__ void stage(const Params& p, unsigned char* xs, int xr
       continue;
     }
     XT v[8];
+    if (PARTS == 3 && p.fast_x && col + 8 <= p.cols) {
 #pragma unroll
-    for (int o = 0; o < 8; ++o) v[o] = col + o < p.cols ? from[o] : from_f32<XT>(0.f);
+      for (int o = 0; o < 8; o += 16 / sizeof(XT)) {
+        const uint4 some = *reinterpret_cast<const uint4*>(from + o);
+        memcpy(v + o, &some, 16);
+      }
+    } else {
+#pragma unroll
+      for (int o = 0; o < 8; ++o) v[o] = col + o < p.cols ? from[o] : from_f32<XT>(0.f);
+    }
     if constexpr (PARTS == 1) {
       memcpy(to, v, 16);
     } else {
@@ -316,7 +332,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) int4_matmul_kernel(const __gri
 #pragma unroll
   for (int tile = 0; tile < TILES; ++tile) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) sums[warp * PLANE + (2 * t + (c & 1)) * PITCH + tile * 16 + g + (c >> 1) * 8] = total[tile][c];
+    for (int c = 0; c < 4; ++c) {
+      const int col = 2 * t + (c & 1);
+      sums[warp * PLANE + col * PITCH + tile * 16 + g + (c >> 1) * 8] = part_sum<PARTS>(total[tile][c], col);
+    }
   }
   __syncthreads();
   for (int i = tid; i < ROWS * tokens; i += kWarps * 32) {
@@ -324,7 +343,6 @@ __global__ void __launch_bounds__(kWarps * 32, 2) int4_matmul_kernel(const __gri
     float v = 0.f;
 #pragma unroll
     for (int part = PARTS - 1; part >= 0; --part) {
-      if (PARTS > 1 && part == 0) v = lower_parts(v);
 #pragma unroll 8
       for (int w = 0; w < kWarps; ++w) v += sums[w * PLANE + (token * PARTS + part) * PITCH + at];
     }
@@ -430,7 +448,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, NT == 1 ? 4 : 2) int4_matmul_r
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int col = nt * 8 + 2 * t + (c & 1), at = warp * 16 + g + (c >> 1) * 8;
-      if (col < tokens * PARTS) sums[col * (kRows + 4) + at] = col % PARTS ? lower_parts(total[nt][c]) : total[nt][c];
+      const float sum = part_sum<PARTS>(total[nt][c], col);  // (not within the branch: 4.7 us a call for 4.5)
+      if (col < tokens * PARTS) sums[col * (kRows + 4) + at] = sum;
     }
   }
   if (split > 1) cluster.sync();

@@ -113,3 +113,25 @@ def test_nan_tokens_of_every_payload(tokens):
         for s in (1.0, float("inf")):
             y = B.int4_matmul(x, packed, torch.full((1, 16), s, device="cuda"), None, 0)
             assert torch.isnan(y[-1]).all() and (y[:-1] == 256 * s).all()
+
+
+@pytest.mark.parametrize("tokens", [1, 3, 10])
+@pytest.mark.parametrize("exponent", [-149, -143, -140, -135, -131, -126, -120, -113, -107, -100, 0, 100, 119])
+def test_float32_tokens_of_every_size_are_multiplied_exactly(tokens, exponent):
+    import differentiable_bcjr_b200 as B
+    rows, cols = 64, 256
+    gen = torch.Generator().manual_seed(tokens)
+    packed = torch.randint(0, 256, (4, 2, 1024), generator=gen, dtype=torch.uint8).cuda()
+    scales = torch.ones(1, rows, device="cuda")
+    w = R.int4_weights(packed, scales, None, rows, cols, 0)
+    x = ((torch.rand(tokens, cols, generator=gen).double() + 1) * 2.0 ** exponent * (1 - 2 * torch.randint(0, 2, (tokens, cols), generator=gen))).float().cuda()
+    y = B.int4_matmul(x, packed, scales, None, 0).double()
+    want, size = x.double() @ w.t(), x.double().abs() @ w.abs().t()
+    # exact products; no more than 64 float32 sums on a value's way, each off by 2^-23 of it or half a smallest number
+    assert ((y - want).abs() <= size * 64 * 2 ** -23 + 64 * 2.0 ** -150).all()
+    # one token value at a time: its product alone, rounded once (28 bits; parts are at most two sums more)
+    x = torch.zeros_like(x)
+    x[:, 77] = (1 + 2.0 ** -23) * 2.0 ** exponent
+    x[-1, 77] = -(2 - 2.0 ** -23) * 2.0 ** exponent
+    y, want = B.int4_matmul(x, packed, scales, None, 0).double(), x.double() @ w.t()
+    assert ((y - want).abs() <= want.abs() * 3 * 2 ** -24).all()
