@@ -4,9 +4,12 @@
 // p and the states are written once, so memory bandwidth bounds it (28 B an
 // element for float32 with 32-bit states, 10.06 B for bf16 with 8-bit ones).
 // Measured: 16.8 M float32 elements with 32-bit states 73.8 us (6.4 TB/s, 98 %
-// of the copy rate); 134 M bf16 elements with 8-bit states 352 us (3.8 TB/s),
-// held up by issuing some 64 instructions an element, nine of them the hash
-// (71 and 361 us without the packed float32 operations on pairs).
+// of the copy rate); 134 M bf16 elements with 8-bit states 352 us (3.8 TB/s; 361
+// without the packed float32 operations on pairs).  These issue 67 instructions
+// an element, nine of them the hash, which alone would take 240 us; the rest is
+// latency that too few warps hide (42 % of them, issue 71 %): the loads of a block
+// wait behind the arithmetic of the one before.  With a count on the device every
+// CTA takes two powers before its first load, 395 us.
 // The flat states are cut into blocks of 256 elements, the blocks that 8-bit
 // scales belong to; a warp takes one block at a time, 8 elements a lane, and
 // finds its tensor by bisection in a table that travels as a kernel

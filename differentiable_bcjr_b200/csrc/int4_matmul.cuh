@@ -21,11 +21,16 @@
 // the CTAs of a cluster split the columns of the matrix and add their sums
 // through distributed shared memory in a fixed order.
 //
-// Measured, device time a call: 8192 x 8192 in groups of 128, one bf16 token 10.8 us
-// (33.6 MB: 3.1 TB/s; reading them alone takes 6.4 us from memory with as many
-// threads), 8 tokens 12.4 us, 32 tokens 22.4 us; 16384 x 8192 in groups of 32, 16 half
-// tokens 34 us.  The integer pipe (masks and shifts) and too few warps to hide
-// latencies bound it, not the matrix instruction (20 % busy) nor memory.
+// Measured, device time a call with the weights in memory (in the L2 cache): 8192 x
+// 8192 in groups of 128, one bf16 token 11.4 us (10.7; 34.6 MB: 3.0 TB/s; reading
+// them alone takes 6.4 us from memory with as many threads), 8 tokens 13.1 (12.4),
+// 32 tokens 22.9 (22.3), one float32 token 13.1 (12.3), ten 23.7 (22.6); 16384 x
+// 8192 in groups of 32, 16 half tokens 36.8 (33.9).  No pipe is full: one token
+// issues half of the time, the integer pipe (masks and shifts) is busy 42 %, the
+// matrix instruction 19 %, and 16 tokens less.  It is latency: two tiles of weights
+// are on their way for a warp, and for several tokens every chunk's staging is
+// waited for.  More than 32 tokens take as many passes over the weights (256
+// tokens 152 us, 2048 tokens 1.0 ms).
 #pragma once
 #include <cooperative_groups.h>
 

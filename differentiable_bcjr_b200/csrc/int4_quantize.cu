@@ -5,11 +5,12 @@
 // word of the packed tile, so a lane reads 16 or 32 contiguous bytes and
 // writes one word, two blocks' loads ahead of the work on them.  Groups of 32,
 // 64 and 128 columns are 4, 8 and 16 neighbouring lanes, their extremes a few
-// shuffles.  Reading w bounds the call (4.5 B a weight for float32 moved in
-// all, 2.5 B for 16-bit types): 2048 x 8192 float32 in groups of 128 takes 14.9
-// us (5.1 TB/s); 16-bit types have the same work for fewer bytes and take as long
-// (17.6 us), waiting for one another's shuffles and reciprocals.  Persistent CTAs
-// with the next blocks' loads on the way were slower (19.3 us).
+// shuffles.  Reading w bounds the call for float32 (4.5 B a weight moved in all):
+// 2048 x 8192 in groups of 128 takes 13.7 us from memory (5.5 TB/s; whole rows,
+// read twice, 18.3).  16-bit types (2.5 B a weight) take 16.2 us, because a lane
+// has eight columns whatever their type: half the bytes on the way for the same
+// shuffles, reciprocals and codes.  Persistent CTAs with the next blocks' loads on
+// the way were slower.
 #include <cmath>
 #include <cstring>
 
@@ -168,8 +169,8 @@ __device__ __forceinline__ void put_word(const Params& p, float (&v)[8], const C
   }
 }
 
-// Blocks that a thread loads before it works on them: two, 2048 x 8192 float32
-// 15.6 us; one 19.2, four 16.3 (fewer warps), eight 24.1.
+// Blocks that a thread loads before it works on them.  Measured when it was chosen
+// (2048 x 8192 float32): two 15.6 us, one 19.2, four 16.3 (fewer warps), eight 24.1.
 constexpr int kAtOnce = 2;
 
 template <typename T, bool ZERO, bool HALF>

@@ -20,10 +20,12 @@
 // the lanes of a gather meet in fewer banks, so both walks together take less
 // than two full ones).
 //
-// Measured, device time a call: 2048 x 8192, k = 2, 2^16 states, one token 12.3 us
-// with a bf16 codebook (its gathers alone, at 3.5 clocks a warp, would take 6.6 us), 18.8 us
-// with a float32 one.  Several tokens of the codebook's own 16-bit type take the
-// kernel of trellis_mma.cuh.
+// Measured, device time a call with the words in memory (in the L2 cache): 2048 x
+// 8192, k = 2, 2^16 states, one token 13.5 us (12.4) with a bf16 codebook (its
+// gathers alone, at 3.5 clocks a warp, would take 6.6 us), 20.0 (19.0) with a float32
+// one, whose halves every CTA copies and walks its rows for one after the other;
+// four bf16 tokens 31.8 (29.5), eight 49.7 (46.0).  Several tokens of the codebook's
+// own 16-bit type take the kernel of trellis_mma.cuh.
 #pragma once
 #include <type_traits>
 

@@ -19,9 +19,11 @@
 // share the rows out by eights; a tile of only eight skips the gathers of its
 // lower half.
 //
-// Measured, device time a call, bf16: 8192 x 2048, k = 4, 2^16 states, 8 tokens
-// 15.2 us (multiply-adds and warp sums: 21.8; the gathers alone 6.6; launch and
-// codebook 4.1), 16 tokens 19.8; 8192 x 8192, k = 2, 2^8 states, 2 tokens 29.2 us.
+// Measured, device time a call with the words in memory (in the L2 cache), bf16:
+// 8192 x 2048, k = 4, 2^16 states, 8 tokens 16.5 us (15.2; multiply-adds and warp
+// sums: 21.8; the gathers alone 6.6; launch and codebook 4.1), 16 tokens 23.6
+// (19.8); 8192 x 8192, k = 2, 2^8 states, 2 tokens 31.4 (29.1).  More than 16 tokens
+// take as many passes over the words (256 tokens of 8192 x 2048: 301 us).
 #pragma once
 #include <cooperative_groups.h>
 

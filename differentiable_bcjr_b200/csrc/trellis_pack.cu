@@ -6,7 +6,8 @@
 // shared memory, and then lane l puts the words of piece l together.  What
 // precedes a piece in the stream are the upper bits of its first state, so no
 // piece waits for another.  Reading the states (4 B a weight) bounds the call:
-// 65536 sequences of 256 states take 14.9 us (4.8 TB/s).
+// 65536 sequences of 256 states take 16.1 us from memory (4.7 TB/s), 9.3 from the
+// L2 cache.
 #include "layer_util.cuh"
 
 namespace {

@@ -94,7 +94,8 @@ bcjr_status bcjr_adamw_step(const bcjr_adamw_tensor* tensors, int n_tensors, int
  * rounded to its type before the codes are taken, and a code is rint(w * (1 /
  * scale)), which differs from the quotient's only next to a tie.  Where the scale is 0
  * the codes are the zero point.  A group that holds a NaN or an infinity gets
- * a scale that is not finite.
+ * a scale that is not finite, and so does one whose range or scale overflows
+ * float32 or the scale's type.
  */
 bcjr_status bcjr_int4_quantize(const void* w, int w_dtype, int rows, int cols, int group_size,
                                void* packed, void* scales, int scale_dtype, uint8_t* zeros,
@@ -135,8 +136,10 @@ bcjr_status bcjr_trellis_pack(const int32_t* states, int state_bits, int k, int 
  * ignored).  group_size: 0 for one scale a row, a multiple of seq_len that
  * divides cols, or a multiple of 16 that divides seq_len.  x and y of x_dtype,
  * codebook [2^state_bits] of codebook_dtype; products and sums in float32 (by the
- * tensor core for several tokens of the codebook's own 16-bit type); y must not
- * overlap any of the others.
+ * tensor core for several tokens of the codebook's own 16-bit type), the sums of
+ * up to 64 columns scaled at once.  A sum of 0 under a scale that is not finite (a
+ * token of zeros) is a NaN, or with 2^16 float32 codewords 0.  y must not overlap
+ * any of the others.
  */
 bcjr_status bcjr_trellis_matmul(const void* x, int x_dtype, int tokens, int rows, int cols,
                                 const uint32_t* packed, const void* codebook, int codebook_dtype,
