@@ -57,7 +57,7 @@ typedef struct {
  *     value of a code is the number it stands for and averages over many
  *     steps keep moving when a step's change is smaller than a code; r > 0
  *     never becomes 0, so that no later update divides by eps alone.
- *     Where v overflows (gradients beyond 2^63), the step of that element is 0 as
+ *     Where v overflows (gradients beyond 2^64), the step of that element is 0 as
  *     with 32 bits; its block's scale of r becomes a NaN, and the block's
  *     parameters with it in the next step.  A gradient that is not finite makes
  *     its own parameter NaN and both scales of its block not finite.
