@@ -9,7 +9,7 @@ extern "C" bcjr_status bcjr_trellis_matmul(const void* x, int x_dtype, int token
                                            int state_bits, int k, int seq_len, const float* scales, int group_size,
                                            void* y, bcjr_stream_t stream) {
   if (!dtype_ok(x_dtype) || !dtype_ok(codebook_dtype) || tokens < 0 || rows < 0 || cols < 1 || seq_len < 1 ||
-      state_bits < 1 || k < 1 || k > state_bits || group_size < 0)
+      state_bits < 1 || k < 1 || k > state_bits || (scales && group_size < 0))
     return BCJR_ERR_INVALID_ARG;
   if (cols % seq_len != 0) return BCJR_ERR_INVALID_ARG;
   // passes of 8 tokens are the second grid dimension; columns and bits are counted in ints
