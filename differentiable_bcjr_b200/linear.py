@@ -81,8 +81,10 @@ class TrellisLinear(torch.nn.Module):
         if group_size is not None:
             parts = w.view(rows, _trellis_groups(cols, seq_len, group_size), -1)
             rms = parts.square().mean(2).sqrt()
-            # squares that leave float32's range are summed in 64 bits; a group of zeros has the scale 0
-            rms = torch.where((rms > 2.0 ** -60) & (rms < 2.0 ** 60), rms, parts.double().square().mean(2).sqrt().float())
+            # squares that leave float32's range are those of parts of the largest; a group of zeros has the scale 0
+            top = parts.abs().amax(2)
+            far = top * (parts / top.clamp(min=2.0 ** -149)[:, :, None]).square().mean(2).sqrt()
+            rms = torch.where((rms > 2.0 ** -60) & (rms < 2.0 ** 60), rms, far)
             w = (parts / torch.where(rms > 0, rms, torch.ones_like(rms))[:, :, None]).view(rows, cols)
             scales = rms.t().contiguous()
         states, _ = viterbi_decode(w.view(-1, seq_len), codebook, state_bits, k)
