@@ -64,7 +64,7 @@ def test_outputs_of_the_products(monkeypatch):
     x, out = fake(buf[:256].view(2, 128)), fake(buf[4096:4096 + 32].view(2, 16))
     scales, packed = fake(buf[1024:1040].view(1, 16)), fake(buf[2048:2304].view(torch.uint8).view(1, 1, 1024))
     zeros = fake(buf[1536:1540].view(torch.uint8).view(1, 16))
-    stream, codebook = fake(buf[3072:3072 + 16 * 9].view(torch.int32).view(16, 9)), fake(buf[8192:8192 + 256])
+    stream, codebook = fake(buf[2560:2560 + 16 * 9].view(torch.int32).view(16, 9)), fake(buf[8192:8192 + 256])
 
     def int4(out):
         return B.int4_matmul(x, packed, scales, zeros, 0, out=out)
